@@ -54,8 +54,9 @@ enum {
     WPATTN_ECUDA = 3,         /* a CUDA runtime call or a kernel launch failed */
     WPATTN_ETIMEOUT = 4,      /* a kernel's bounded wait ran out (see wpattn_device_status) */
     WPATTN_EWORKSPACE = 5,    /* workspace null or smaller than wpattn_decode_workspace_size */
-    WPATTN_EINDEX = 6         /* a device-side index was out of range (block-table entry outside
+    WPATTN_EINDEX = 6,        /* a device-side index was out of range (block-table entry outside
                                  the pool, negative key position); see wpattn_device_status */
+    WPATTN_EPAGES = 7         /* the pool had no free page left; see wpattn_device_status */
 };
 
 /*
@@ -496,10 +497,173 @@ WPATTN_API int wpattn_merge_lse(const void *outs, const float *lses, int32_t R, 
                   int32_t head_dim, void *out, float *lse, void *cuda_stream);
 
 /*
+ * Prefill of a ragged batch of chunks over a paged KV cache: the new tokens
+ * of B sequences, any number of them each, attend their sequence's cached
+ * keys, their own among them (write those first: wpattn_append_paged).  The
+ * chunks of a long prompt, drafts to be checked and single tokens may share a
+ * call.
+ *   q          : bf16 device [T, Hq, D], T = sum of q_len; the rows of sequence
+ *                0, then of sequence 1, ...
+ *   k_pages, v_pages, num_pages, page_size, block_table, max_pages_per_seq:
+ *                as for wpattn_decode_paged (page_size 8, 16 or a multiple of
+ *                32; a table entry outside the pool: page 0 is read in its
+ *                place and WPATTN_EINDEX recorded).
+ *   q_len_host : host int32 [B], new tokens of each sequence, >= 0
+ *   kv_len_host: host int32 [B], its cached keys, 0 <= kv_len <=
+ *                max_pages_per_seq * page_size.  Query t sits at kv_len - q_len
+ *                + t, key j at j; one before key 0 gets out = 0, lse = -inf.
+ *   out        : bf16 device [T, Hq, D];  lse: fp32 device [T, Hq] or NULL
+ *   workspace  : device, 256-byte aligned, at least
+ *                wpattn_prefill_paged_workspace_size(...) bytes (else
+ *                WPATTN_EWORKSPACE); may be NULL when that is 0.  Two calls
+ *                that can overlap on the GPU need one each.
+ * Rows of the pools behind a sequence's last key hold anything (NaN
+ * included); a non-finite V among a sequence's keys may reach queries of the
+ * chunk before it.  Requires D in {64, 128}, Hq / Hkv <= 128, B <= 1024,
+ * max_pages_per_seq * page_size <= 2^30, num_pages * page_size < 2^31.
+ */
+WPATTN_API int wpattn_prefill_paged(const wpattn_window *w,
+                  const void *q, const void *k_pages, const void *v_pages,
+                  int32_t num_pages, int32_t page_size,
+                  const int32_t *block_table, int32_t max_pages_per_seq,
+                  const int32_t *q_len_host, const int32_t *kv_len_host,
+                  int32_t B, int32_t Hq, int32_t Hkv, float softmax_scale,
+                  void *out, float *lse,
+                  void *workspace, size_t workspace_bytes,
+                  void *cuda_stream);
+
+/* Workspace bytes wpattn_prefill_paged needs for these lengths on the current
+ * device (0 on bad arguments, and when no key range is split). */
+WPATTN_API size_t wpattn_prefill_paged_workspace_size(const wpattn_window *w,
+                  const int32_t *q_len_host, const int32_t *kv_len_host,
+                  int32_t B, int32_t Hq, int32_t Hkv);
+
+/*
+ * RoPE with positions along several axes (time, height and width of image or
+ * video tokens): as wpattn_rope, but pair p of token t turns by
+ * positions[pair_axis[p] * pos_stride + t] * rope_base^(-2p/D).
+ *   q, k       : bf16 device, token t's heads at q + t * q_stride (elements; a
+ *                multiple of 8, >= Hq * head_dim), so that they may be slices
+ *                of one projection; k may be NULL (k_out too)
+ *   q_out, k_out: bf16 device [tokens, H, head_dim]; may be q, k when those are
+ *                contiguous
+ *   positions  : device int32 [axes, pos_stride], pos_stride >= tokens (any when
+ *                axes = 1)
+ *   pair_axis_host: host uint8 [head_dim / 2], each < axes; NULL = all 0
+ *   inverse    : 1 turns by minus the angle: the transpose, which is the
+ *                gradient of the rotation (and undoes it up to rounding)
+ * 1 <= axes <= 4.  All pointers of tensors 16-byte aligned.
+ */
+WPATTN_API int wpattn_rope_axes(const void *q, int64_t q_stride, void *q_out,
+                  const void *k, int64_t k_stride, void *k_out,
+                  int32_t tokens, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                  const int32_t *positions, int64_t pos_stride, int32_t axes,
+                  const uint8_t *pair_axis_host, double rope_base, int32_t inverse,
+                  void *cuda_stream);
+
+/*
+ * A step's new tokens into a paged KV cache, rotated on the way: k and v of
+ * sequence b's new_len tokens become its cache rows kv_len - new_len ..
+ * kv_len - 1 (row j is row j % page_size of page block_table[b, j /
+ * page_size]); q is rotated beside them, in the same launch.
+ *   k, v       : bf16 device, token t's heads at k + t * k_stride (elements, a
+ *                multiple of 8), tokens packed as for wpattn_prefill_paged
+ *   q, q_out   : both NULL, or bf16 device, q_out [T, Hq, head_dim]
+ *   new_len_host, kv_len_host: host int32 [B], 0 <= new_len <= kv_len <=
+ *                max_pages_per_seq * page_size; kv_len counts the new tokens
+ *   rope_base  : 0 = the tokens are stored as they are (q, positions and
+ *                pair_axis_host NULL); otherwise k and q turn as in
+ *                wpattn_rope_axes, by positions (NULL: the token's cache row;
+ *                axes = 1)
+ * A table entry outside the pool: the token is not stored and WPATTN_EINDEX
+ * recorded.  Nothing else of the pools is written.  B <= 1024; the page sizes
+ * of wpattn_decode_paged.
+ */
+WPATTN_API int wpattn_append_paged(const void *k, int64_t k_stride,
+                  const void *v, int64_t v_stride,
+                  const void *q, int64_t q_stride, void *q_out,
+                  void *k_pages, void *v_pages, int32_t num_pages, int32_t page_size,
+                  const int32_t *block_table, int32_t max_pages_per_seq,
+                  const int32_t *new_len_host, const int32_t *kv_len_host,
+                  int32_t B, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                  const int32_t *positions, int64_t pos_stride, int32_t axes,
+                  const uint8_t *pair_axis_host, double rope_base,
+                  void *cuda_stream);
+
+/*
+ * Page maintenance.  A cache is a block table [num_rows, max_pages] (device
+ * int32, one row per sequence slot, -1 = no page), refs [num_pages] (device
+ * int32: how many table entries name each page, 0 = free) and any number of
+ * pools (the K and V pools of every layer, all with the same pages): a host
+ * array of up to 256 device pointers, 16-byte aligned, a page being page_bytes
+ * (a multiple of 16) in each.  Only full pages are shared between rows, so
+ * a sequence always owns the page it appends to.  Free pages are taken lowest
+ * index first: results do not depend on timing.  Calls on one cache are
+ * ordered by its stream; at most 1024 rows per call.  Rows named twice, rows
+ * outside the table and lengths outside it are WPATTN_EINVAL.
+ *
+ * wpattn_pages_copy: page src[i] of every pool onto page dst[i], i < n (device
+ * int32 [n] each).  No page may be written that the call also reads or writes
+ * elsewhere.  An index outside the pool: skipped, WPATTN_EINDEX recorded.
+ */
+WPATTN_API int wpattn_pages_copy(void *const *pools_host, int32_t n_pools, int32_t num_pages,
+                  int64_t page_bytes, const int32_t *src, const int32_t *dst, int32_t n,
+                  void *cuda_stream);
+
+/* Workspace bytes of wpattn_pages_fork and wpattn_pages_compact (device,
+ * 16-byte aligned). */
+WPATTN_API size_t wpattn_pages_workspace_size(int32_t num_pages);
+
+/*
+ * Fork i makes row dst_rows[i] (unused until now, its old entries are
+ * overwritten) a copy of row src_rows[i], which holds len[i] keys: full pages
+ * are shared, and the begun page's keys (row_bytes each) are copied in every
+ * pool into a page of the fork's own.  A row may be the source of any number
+ * of forks, but no row both source and destination.  Without enough free pages
+ * the last forks' begun pages stay -1 and WPATTN_EPAGES is recorded.
+ */
+WPATTN_API int wpattn_pages_fork(void *const *pools_host, int32_t n_pools, int32_t num_pages,
+                  int32_t page_size, int64_t row_bytes,
+                  int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *refs,
+                  const int32_t *src_rows_host, const int32_t *dst_rows_host,
+                  const int32_t *len_host, int32_t n,
+                  void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * The rows' pages for len[i] keys lose a reference each, and the entries
+ * become -1.  An entry outside the pool or a page that is free already:
+ * WPATTN_EINDEX recorded.
+ */
+WPATTN_API int wpattn_pages_free(int32_t num_pages, int32_t page_size,
+                  int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *refs,
+                  const int32_t *rows_host, const int32_t *len_host, int32_t n, void *cuda_stream);
+
+/*
+ * Row i grows from len[i] to new_len[i] keys: the pages it lacks are the lowest
+ * free ones, row by row.  Without enough of them the last entries stay -1
+ * and WPATTN_EPAGES is recorded.
+ */
+WPATTN_API int wpattn_pages_extend(int32_t num_pages, int32_t page_size,
+                  int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *refs,
+                  const int32_t *rows_host, const int32_t *len_host, const int32_t *new_len_host,
+                  int32_t n, void *cuda_stream);
+
+/*
+ * Moves the pages in use into the first slots of the pools, n of them: the k-th
+ * page in use at or behind slot n goes to the k-th free slot before it.  refs
+ * and every entry of the table (`entries` of them, -1 and others outside the
+ * pool left alone) follow.  live: device int32 [1], gets n, or NULL.
+ */
+WPATTN_API int wpattn_pages_compact(void *const *pools_host, int32_t n_pools, int32_t num_pages,
+                  int64_t page_bytes, int32_t *block_table, int64_t entries, int32_t *refs,
+                  int32_t *live, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
  * Synchronises `cuda_stream`, then reads and clears the current device's
  * kernel status word.  Returns WPATTN_OK, WPATTN_ETIMEOUT (a kernel gave up a
  * bounded wait; its outputs are undefined), WPATTN_EINDEX (a kernel met an
- * out-of-range device-side index; its outputs are undefined) or WPATTN_ECUDA.
+ * out-of-range device-side index; its outputs are undefined), WPATTN_EPAGES
+ * (a pool had no free page left) or WPATTN_ECUDA.
  */
 WPATTN_API int wpattn_device_status(void *cuda_stream);
 

@@ -13,7 +13,9 @@ Entry points (same names as the C ABI, without the ``wpattn_`` prefix):
 ``kcache_to_pairmajor``, ``decode_positions``, ``decode_paged``, ``prefill_masked``,
 ``pack_block_mask``, ``rope``, ``rope_qk``, ``prefill_rope``, ``decode_rope``,
 ``prefill_positions``, ``decode_shard``, ``merge_lse``, ``decode_workspace_size``,
-``decode_noalloc``, ``pruned_fraction``, ``thresholds``, ``device_status``.
+``decode_noalloc``, ``pruned_fraction``, ``thresholds``, ``device_status``.  For a paged cache
+(``paged`` module): ``prefill_paged``, ``append_paged``, ``rope_axes``, ``pages_copy``,
+``pages_fork``, ``pages_free``, ``pages_extend``, ``pages_compact``.
 
 Calls are asynchronous on the given stream (torch's current stream by
 default).  Every wait inside a kernel is bounded; when one runs out, the
@@ -33,7 +35,7 @@ from dataclasses import dataclass
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libwpattn.so")
 
-OK, EINVAL, EUNSUPPORTED, ECUDA, ETIMEOUT, EWORKSPACE, EINDEX = range(7)
+OK, EINVAL, EUNSUPPORTED, ECUDA, ETIMEOUT, EWORKSPACE, EINDEX, EPAGES = range(8)
 
 
 class WpattnError(RuntimeError):
@@ -114,6 +116,24 @@ def lib() -> ctypes.CDLL:
         L.wpattn_merge_lse.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp]
         L.wpattn_decode_paged.argtypes = [wp, vp, vp, vp, i32, i32, vp, i32, i32p, i32p, vp, i64,
                                           i32, i32, i32, f32, vp, vp, vp, ctypes.c_size_t, vp]
+        u8p, vpp, f64, sz = (ctypes.POINTER(ctypes.c_uint8), ctypes.POINTER(vp), ctypes.c_double,
+                             ctypes.c_size_t)
+        L.wpattn_prefill_paged.argtypes = [wp, vp, vp, vp, i32, i32, vp, i32, i32p, i32p, i32, i32, i32,
+                                           f32, vp, vp, vp, sz, vp]
+        L.wpattn_prefill_paged_workspace_size.restype = sz
+        L.wpattn_prefill_paged_workspace_size.argtypes = [wp, i32p, i32p, i32, i32, i32]
+        L.wpattn_rope_axes.argtypes = [vp, i64, vp, vp, i64, vp, i32, i32, i32, i32, vp, i64, i32, u8p,
+                                       f64, i32, vp]
+        L.wpattn_append_paged.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, vp, i32, i32p,
+                                          i32p, i32, i32, i32, i32, vp, i64, i32, u8p, f64, vp]
+        L.wpattn_pages_copy.argtypes = [vpp, i32, i32, i64, vp, vp, i32, vp]
+        L.wpattn_pages_workspace_size.restype = sz
+        L.wpattn_pages_workspace_size.argtypes = [i32]
+        L.wpattn_pages_fork.argtypes = [vpp, i32, i32, i32, i64, vp, i32, i32, vp, i32p, i32p, i32p, i32,
+                                        vp, sz, vp]
+        L.wpattn_pages_free.argtypes = [i32, i32, vp, i32, i32, vp, i32p, i32p, i32, vp]
+        L.wpattn_pages_extend.argtypes = [i32, i32, vp, i32, i32, vp, i32p, i32p, i32p, i32, vp]
+        L.wpattn_pages_compact.argtypes = [vpp, i32, i32, i64, vp, i64, vp, vp, vp, sz, vp]
         L.wpattn_device_status.argtypes = [vp]
         L.wpattn_selftest_wait_timeout.argtypes = [vp]
         L.wpattn_strerror.restype = ctypes.c_char_p
@@ -707,3 +727,16 @@ def selftest_wait_timeout(stream=None) -> None:
 
 def default_scale(D: int) -> float:
     return 1.0 / math.sqrt(D)
+
+
+_PAGED = ("append_paged", "pages_compact", "pages_copy", "pages_extend", "pages_fork", "pages_free",
+          "prefill_paged", "prefill_paged_workspace_size", "rope_axes")
+
+
+def __getattr__(name):
+    """The paged-cache operators, loaded (with torch) on first use."""
+    if name not in _PAGED:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import paged
+    globals().update({n: getattr(paged, n) for n in _PAGED})
+    return globals()[name]

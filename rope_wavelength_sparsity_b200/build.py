@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libwpattn.so")
 SOURCES = ["api.cu", "planner.cpp"]
 DEPS = SOURCES + ["device_util.cuh", "decode_kernels.cuh", "prefill_kernel.cuh", "rope_kernels.cuh",
-                  "planner.h"]
+                  "paged_api.cuh", "paged_kernels.cuh", "prefill_paged_kernel.cuh", "planner.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

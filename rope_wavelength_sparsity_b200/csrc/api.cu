@@ -339,6 +339,7 @@ const char* wpattn_strerror(int code) {
     case WPATTN_ETIMEOUT: return "a kernel gave up a bounded wait";
     case WPATTN_EWORKSPACE: return "workspace missing or too small";
     case WPATTN_EINDEX: return "a device-side index (page or position) was out of range";
+    case WPATTN_EPAGES: return "no free page was left";
     default: return "unknown status code";
   }
 }
@@ -977,3 +978,5 @@ int wpattn_device_status(void* cuda_stream) {
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

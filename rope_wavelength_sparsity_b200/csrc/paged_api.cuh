@@ -1,0 +1,392 @@
+// C ABI of the paged-cache operators (declarations and contracts in
+// include/wpattn.h): argument checks and launches.  Included by api.cu.
+#pragma once
+
+#include "paged_kernels.cuh"
+#include "prefill_paged_kernel.cuh"
+
+namespace wpattn {
+namespace {
+
+int launched() { return cudaGetLastError() == cudaSuccess ? WPATTN_OK : WPATTN_ECUDA; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// a 32-key block is one page, a part of one page, or a whole number of pages
+bool page_size_ok(int page_size) {
+  return page_size == 8 || page_size == 16 || (page_size > 0 && page_size % 32 == 0);
+}
+
+template <int MAXB>
+int launch_rope_axes(AxesParams<MAXB>& p, int D, int num_sms, cudaStream_t st) {
+  uint64_t per = 0;
+  for (int s = 0; s < p.nseg; ++s) per += (p.seg[s].H + 3) / 4;
+  const uint64_t items = static_cast<uint64_t>(p.tokens) * (D / 16) * per;
+  if (items == 0) return WPATTN_OK;
+  const unsigned grid = static_cast<unsigned>(std::min<uint64_t>((items + 255) / 256, static_cast<uint64_t>(num_sms) * 8));
+  if (D == 64) rope_axes_kernel<64, MAXB><<<grid, 256, 0, st>>>(p);
+  else rope_axes_kernel<128, MAXB><<<grid, 256, 0, st>>>(p);
+  return launched();
+}
+
+// arguments that the rotating entry points share
+bool axes_ok(int D, int64_t tokens, const int32_t* positions, int64_t pos_stride, int32_t axes,
+             const uint8_t* pair_axis, double base) {
+  if (!(base > 1.0) || std::isinf(base) || axes < 1 || axes > kMaxAxes) return false;
+  if (!positions && axes != 1) return false;
+  if (positions && (!aligned4(positions) || (axes > 1 && pos_stride < tokens))) return false;
+  for (int i = 0; pair_axis && i < D / 2; ++i)
+    if (pair_axis[i] >= axes) return false;
+  return true;
+}
+
+template <int MAXB>
+void set_axes(AxesParams<MAXB>& p, int D, const int32_t* positions, int64_t pos_stride, int32_t axes,
+              const uint8_t* pair_axis, double base) {
+  for (int i = 0; i < D / 2; ++i) p.axis[i] = pair_axis ? pair_axis[i] : 0;
+  p.pos = positions;
+  p.pos_stride = pos_stride;
+  p.axes = axes;
+  rope_thetas(base, D, p.theta);
+}
+
+// pools of a page operator: every pointer present and 16-byte aligned, a page a multiple of 16 bytes
+int set_pools(PagePools* out, void* const* pools, int32_t n_pools, int64_t page_bytes) {
+  if (n_pools < 0 || (n_pools > 0 && !pools) || page_bytes <= 0 || page_bytes % 16 != 0) return WPATTN_EINVAL;
+  if (n_pools > kMaxPools) return WPATTN_EUNSUPPORTED;
+  std::memset(out, 0, sizeof *out);
+  out->n = n_pools;
+  for (int i = 0; i < n_pools; ++i) {
+    if (!pools[i] || !aligned16(pools[i])) return WPATTN_EINVAL;
+    out->pool[i] = static_cast<uint8_t*>(pools[i]);
+  }
+  return WPATTN_OK;
+}
+
+// 1 <= n <= kPageRows rows named once each, inside the table; sorted into `sorted`
+bool rows_ok(const int32_t* rows, int32_t n, int32_t num_rows, int32_t (&sorted)[kPageRows]) {
+  std::copy(rows, rows + n, sorted);
+  std::sort(sorted, sorted + n);
+  return sorted[0] >= 0 && sorted[n - 1] < num_rows && std::adjacent_find(sorted, sorted + n) == sorted + n;
+}
+
+template <int MAXB>
+int append_impl(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                int64_t q_stride, void* q_out, void* k_pages, void* v_pages, int32_t num_pages,
+                int32_t page_size, const int32_t* block_table, int32_t max_pages, const int32_t* new_len,
+                const int32_t* kv_len, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t tokens,
+                const int32_t* positions, int64_t pos_stride, int32_t axes, const uint8_t* pair_axis,
+                double base, int num_sms, cudaStream_t st) {
+  AxesParams<MAXB> p;
+  std::memset(&p, 0, sizeof p);
+  p.tokens = tokens;
+  p.sign = 1.f;
+  p.seg[0] = AxesSegment{static_cast<const uint16_t*>(k), static_cast<uint16_t*>(k_pages), k_stride, Hkv, base != 0.0, 1};
+  p.seg[1] = AxesSegment{static_cast<const uint16_t*>(v), static_cast<uint16_t*>(v_pages), v_stride, Hkv, 0, 1};
+  p.nseg = 2;
+  if (q) p.seg[p.nseg++] = AxesSegment{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(q_out), q_stride, Hq, 1, 0};
+  if (base != 0.0) set_axes(p, D, positions, pos_stride, axes, pair_axis, base);
+  p.block_table = block_table;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  for (int b = 0; b < B; ++b) {
+    p.start[b + 1] = p.start[b] + new_len[b];
+    p.kv_len[b] = kv_len[b];
+  }
+  return launch_rope_axes(p, D, num_sms, st);
+}
+
+// sum of B lengths of at least 0; -1 when one is negative or the sum passes int32
+int64_t sum_lengths(const int32_t* len, int32_t B) {
+  int64_t sum = 0;
+  for (int b = 0; b < B; ++b) {
+    if (len[b] < 0) return -1;
+    sum += len[b];
+  }
+  return sum <= INT32_MAX ? sum : -1;
+}
+
+}  // namespace
+}  // namespace wpattn
+
+extern "C" {
+
+int wpattn_rope_axes(const void* q, int64_t q_stride, void* q_out, const void* k, int64_t k_stride,
+                     void* k_out, int32_t tokens, int32_t Hq, int32_t Hkv, int32_t head_dim,
+                     const int32_t* positions, int64_t pos_stride, int32_t axes, const uint8_t* pair_axis_host,
+                     double rope_base, int32_t inverse, void* cuda_stream) {
+  if (tokens < 0 || Hq <= 0 || (k && Hkv <= 0) || (!k != !k_out)) return WPATTN_EINVAL;
+  if (head_dim != 64 && head_dim != 128) return WPATTN_EUNSUPPORTED;
+  if (!positions || (inverse != 0 && inverse != 1) ||
+      !axes_ok(head_dim, tokens, positions, pos_stride, axes, pair_axis_host, rope_base))
+    return WPATTN_EINVAL;
+  if (tokens == 0) return WPATTN_OK;
+  if (!q || !q_out || !aligned16(q) || !aligned16(q_out) || q_stride < int64_t(Hq) * head_dim || q_stride % 8)
+    return WPATTN_EINVAL;
+  if (k && (!aligned16(k) || !aligned16(k_out) || k_stride < int64_t(Hkv) * head_dim || k_stride % 8))
+    return WPATTN_EINVAL;
+  DeviceInfo* dev = nullptr;
+  int rc;
+  if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
+  AxesParams<1> p;
+  std::memset(&p, 0, sizeof p);
+  p.tokens = tokens;
+  p.sign = inverse ? -1.f : 1.f;
+  set_axes(p, head_dim, positions, pos_stride, axes, pair_axis_host, rope_base);
+  p.seg[0] = AxesSegment{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(q_out), q_stride, Hq, 1, 0};
+  p.nseg = 1;
+  if (k) p.seg[p.nseg++] = AxesSegment{static_cast<const uint16_t*>(k), static_cast<uint16_t*>(k_out), k_stride, Hkv, 1, 0};
+  return launch_rope_axes(p, head_dim, dev->num_sms, static_cast<cudaStream_t>(cuda_stream));
+}
+
+int wpattn_append_paged(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                        int64_t q_stride, void* q_out, void* k_pages, void* v_pages, int32_t num_pages,
+                        int32_t page_size, const int32_t* block_table, int32_t max_pages_per_seq,
+                        const int32_t* new_len_host, const int32_t* kv_len_host, int32_t B, int32_t Hq,
+                        int32_t Hkv, int32_t head_dim, const int32_t* positions, int64_t pos_stride,
+                        int32_t axes, const uint8_t* pair_axis_host, double rope_base, void* cuda_stream) {
+  if (B < 0 || Hkv <= 0 || (!q != !q_out) || (q && Hq <= 0)) return WPATTN_EINVAL;
+  if (head_dim != 64 && head_dim != 128) return WPATTN_EUNSUPPORTED;
+  if (rope_base == 0.0 && (q || positions || pair_axis_host)) return WPATTN_EINVAL;  // nothing would turn them
+  if (!page_size_ok(page_size) || B > kPagedMaxB) return WPATTN_EUNSUPPORTED;
+  if (B == 0) return WPATTN_OK;
+  if (!new_len_host || !kv_len_host || num_pages <= 0 || max_pages_per_seq <= 0) return WPATTN_EINVAL;
+  const int64_t tokens = sum_lengths(new_len_host, B), cap = int64_t(max_pages_per_seq) * page_size;
+  if (tokens < 0) return WPATTN_EINVAL;
+  for (int b = 0; b < B; ++b)
+    if (kv_len_host[b] < new_len_host[b] || kv_len_host[b] > cap) return WPATTN_EINVAL;
+  if (rope_base != 0.0 && !axes_ok(head_dim, tokens, positions, pos_stride, axes, pair_axis_host, rope_base))
+    return WPATTN_EINVAL;
+  if (tokens == 0) return WPATTN_OK;
+  if (!k || !v || !k_pages || !v_pages || !block_table || !aligned4(block_table)) return WPATTN_EINVAL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      (q && (!aligned16(q) || !aligned16(q_out))))
+    return WPATTN_EINVAL;
+  const int64_t kv_row = int64_t(Hkv) * head_dim, q_row = int64_t(Hq) * head_dim;
+  if (k_stride < kv_row || v_stride < kv_row || (k_stride | v_stride) % 8 || (q && (q_stride < q_row || q_stride % 8)))
+    return WPATTN_EINVAL;
+  DeviceInfo* dev = nullptr;
+  int rc;
+  if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
+  const auto impl = B <= 64 ? append_impl<64> : append_impl<kPagedMaxB>;
+  return impl(k, k_stride, v, v_stride, q, q_stride, q_out, k_pages, v_pages, num_pages, page_size, block_table,
+              max_pages_per_seq, new_len_host, kv_len_host, B, Hq, Hkv, head_dim, static_cast<int32_t>(tokens),
+              positions, pos_stride, axes, pair_axis_host, rope_base, dev->num_sms,
+              static_cast<cudaStream_t>(cuda_stream));
+}
+
+size_t wpattn_prefill_paged_workspace_size(const wpattn_window* w, const int32_t* q_len_host,
+                                           const int32_t* kv_len_host, int32_t B, int32_t Hq, int32_t Hkv) {
+  (void)w; (void)q_len_host; (void)kv_len_host; (void)B; (void)Hq; (void)Hkv;
+  return 0;
+}
+
+int wpattn_prefill_paged(const wpattn_window* w, const void* q, const void* k_pages, const void* v_pages,
+                         int32_t num_pages, int32_t page_size, const int32_t* block_table,
+                         int32_t max_pages_per_seq, const int32_t* q_len_host, const int32_t* kv_len_host,
+                         int32_t B, int32_t Hq, int32_t Hkv, float softmax_scale, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  WindowPlan plan;
+  int rc = make_window_plan(w, &plan);
+  if (rc != WPATTN_OK) return rc;
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || (Hq % Hkv) != 0 || num_pages <= 0 || max_pages_per_seq <= 0)
+    return WPATTN_EINVAL;
+  if (!(softmax_scale == softmax_scale)) return WPATTN_EINVAL;  // NaN
+  if ((plan.D != 64 && plan.D != 128) || !page_size_ok(page_size) || B > kPagedMaxB || Hq / Hkv > 128)
+    return WPATTN_EUNSUPPORTED;
+  if (B == 0) return WPATTN_OK;
+  if (!q_len_host || !kv_len_host) return WPATTN_EINVAL;
+  const int64_t tokens = sum_lengths(q_len_host, B), cap = int64_t(max_pages_per_seq) * page_size;
+  if (tokens < 0) return WPATTN_EINVAL;
+  for (int b = 0; b < B; ++b)
+    if (kv_len_host[b] < 0 || kv_len_host[b] > cap) return WPATTN_EINVAL;
+  if (tokens == 0) return WPATTN_OK;
+  if (!q || !out || !k_pages || !v_pages || !block_table || !aligned4(block_table)) return WPATTN_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_pages) || !aligned16(v_pages)) return WPATTN_EINVAL;
+  if (cap > (int64_t(1) << 30) || int64_t(num_pages) * page_size >= (int64_t(1) << 31)) return WPATTN_EUNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
+  (void)workspace; (void)workspace_bytes;
+  PrefillPagedParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k_pages);
+  p.v = static_cast<const uint16_t*>(v_pages);
+  p.block_table = block_table;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.num_pages = num_pages; p.page_size = page_size; p.max_pages = max_pages_per_seq;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(plan.D));
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  for (int i = 0; i < 64; ++i) p.T[i] = plan.T[i] > INT32_MAX ? INT32_MAX : static_cast<int>(plan.T[i]);
+  for (int b = 0; b < B; ++b) {
+    p.q_start[b + 1] = p.q_start[b] + q_len_host[b];
+    p.kv_len[b] = kv_len_host[b];
+  }
+  const int64_t blocks = (tokens * Hq + 7) / 8;
+  if (blocks > INT32_MAX) return WPATTN_EUNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (plan.D == 64) prefill_paged_kernel<64><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
+  else prefill_paged_kernel<128><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
+  return launched();
+}
+
+int wpattn_pages_copy(void* const* pools_host, int32_t n_pools, int32_t num_pages, int64_t page_bytes,
+                      const int32_t* src, const int32_t* dst, int32_t n, void* cuda_stream) {
+  CopyParams p;
+  int rc = set_pools(&p.pools, pools_host, n_pools, page_bytes);
+  if (rc != WPATTN_OK) return rc;
+  if (n < 0 || num_pages <= 0) return WPATTN_EINVAL;
+  if (n == 0 || n_pools == 0) return WPATTN_OK;
+  if (!src || !dst || !aligned4(src) || !aligned4(dst)) return WPATTN_EINVAL;
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
+  p.src = src; p.dst = dst; p.n = n; p.num_pages = num_pages; p.page_bytes = page_bytes;
+  const dim3 grid(std::min(n, std::max(1, dev->num_sms * 8 / n_pools)), n_pools);
+  copy_pages_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(cuda_stream)>>>(p);
+  return launched();
+}
+
+size_t wpattn_pages_workspace_size(int32_t num_pages) {
+  return num_pages > 0 ? (static_cast<size_t>(num_pages) * 2 + 2) * 4 + 4 * kPageRows : 0;
+}
+
+int wpattn_pages_fork(void* const* pools_host, int32_t n_pools, int32_t num_pages, int32_t page_size,
+                      int64_t row_bytes, int32_t* block_table, int32_t num_rows, int32_t max_pages,
+                      int32_t* refs, const int32_t* src_rows_host, const int32_t* dst_rows_host,
+                      const int32_t* len_host, int32_t n, void* workspace, size_t workspace_bytes,
+                      void* cuda_stream) {
+  if (page_size <= 0 || row_bytes <= 0 || row_bytes % 16) return WPATTN_EINVAL;
+  ForkParams p;
+  std::memset(&p, 0, sizeof p);
+  int rc = set_pools(&p.pools, pools_host, n_pools, row_bytes * page_size);
+  if (rc != WPATTN_OK) return rc;
+  if (n < 0 || num_pages <= 0 || num_rows <= 0 || max_pages <= 0) return WPATTN_EINVAL;
+  if (n > kPageRows) return WPATTN_EUNSUPPORTED;
+  if (n == 0) return WPATTN_OK;
+  if (!block_table || !refs || !src_rows_host || !dst_rows_host || !len_host || !aligned4(block_table) ||
+      !aligned4(refs))
+    return WPATTN_EINVAL;
+  int32_t dsts[kPageRows];
+  if (!rows_ok(dst_rows_host, n, num_rows, dsts)) return WPATTN_EINVAL;
+  int begun = 0, most = 0;
+  for (int i = 0; i < n; ++i) {
+    if (src_rows_host[i] < 0 || src_rows_host[i] >= num_rows || len_host[i] < 0 ||
+        len_host[i] > int64_t(max_pages) * page_size ||
+        std::binary_search(dsts, dsts + n, src_rows_host[i]))
+      return WPATTN_EINVAL;
+    p.src[i] = src_rows_host[i];
+    p.dst[i] = dst_rows_host[i];
+    p.len[i] = len_host[i];
+    p.rank[i] = len_host[i] % page_size ? begun++ : -1;
+    most = std::max(most, len_host[i] % page_size);
+  }
+  if (!workspace || workspace_bytes < wpattn_pages_workspace_size(num_pages)) return WPATTN_EWORKSPACE;
+  if (!aligned16(workspace)) return WPATTN_EINVAL;
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  int32_t* list = static_cast<int32_t*>(workspace);
+  if (begun > 0) {
+    find_free_pages_kernel<<<1, kScanThreads, 0, st>>>(refs, num_pages, list, begun);
+    if ((rc = launched()) != WPATTN_OK) return rc;
+  }
+  p.table = block_table; p.refs = refs; p.list = list;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size; p.n = n;
+  p.row_bytes = row_bytes;
+  // 16 KB of copies a block, at most about eight blocks an SM
+  const int64_t per_fork = row_bytes * most * n_pools;
+  const int64_t x = std::max<int64_t>(1, std::min<int64_t>((per_fork + 16383) / 16384, int64_t(dev->num_sms) * 8 / n + 1));
+  fork_kernel<<<dim3(static_cast<unsigned>(x), n), 256, 0, st>>>(p);
+  return launched();
+}
+
+int wpattn_pages_free(int32_t num_pages, int32_t page_size, int32_t* block_table, int32_t num_rows,
+                      int32_t max_pages, int32_t* refs, const int32_t* rows_host, const int32_t* len_host,
+                      int32_t n, void* cuda_stream) {
+  if (n < 0 || num_pages <= 0 || page_size <= 0 || num_rows <= 0 || max_pages <= 0) return WPATTN_EINVAL;
+  if (n > kPageRows) return WPATTN_EUNSUPPORTED;
+  if (n == 0) return WPATTN_OK;
+  int32_t sorted[kPageRows];
+  if (!block_table || !refs || !rows_host || !len_host || !aligned4(block_table) || !aligned4(refs) ||
+      !rows_ok(rows_host, n, num_rows, sorted))
+    return WPATTN_EINVAL;
+  RowsParams p;
+  std::memset(&p, 0, sizeof p);
+  int longest = 0;
+  for (int i = 0; i < n; ++i) {
+    if (len_host[i] < 0 || len_host[i] > int64_t(max_pages) * page_size) return WPATTN_EINVAL;
+    p.row[i] = rows_host[i];
+    p.len[i] = len_host[i];
+    longest = std::max(longest, len_host[i]);
+  }
+  if (longest == 0) return WPATTN_OK;
+  DeviceInfo* dev = nullptr;
+  const int rc = device_info(&dev);
+  if (rc != WPATTN_OK) return rc;
+  p.table = block_table; p.refs = refs;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size; p.n = n;
+  const int pages = (longest + page_size - 1) / page_size;
+  free_kernel<<<dim3((pages + 255) / 256, n), 256, 0, static_cast<cudaStream_t>(cuda_stream)>>>(p);
+  return launched();
+}
+
+int wpattn_pages_extend(int32_t num_pages, int32_t page_size, int32_t* block_table, int32_t num_rows,
+                        int32_t max_pages, int32_t* refs, const int32_t* rows_host, const int32_t* len_host,
+                        const int32_t* new_len_host, int32_t n, void* cuda_stream) {
+  if (n < 0 || num_pages <= 0 || page_size <= 0 || num_rows <= 0 || max_pages <= 0) return WPATTN_EINVAL;
+  if (n > kPageRows) return WPATTN_EUNSUPPORTED;
+  if (n == 0) return WPATTN_OK;
+  int32_t sorted[kPageRows];
+  if (!block_table || !refs || !rows_host || !len_host || !new_len_host || !aligned4(block_table) ||
+      !aligned4(refs) || !rows_ok(rows_host, n, num_rows, sorted))
+    return WPATTN_EINVAL;
+  ExtendParams p;
+  std::memset(&p, 0, sizeof p);
+  int64_t want = 0;
+  for (int i = 0; i < n; ++i) {
+    if (len_host[i] < 0 || new_len_host[i] < len_host[i] || new_len_host[i] > int64_t(max_pages) * page_size)
+      return WPATTN_EINVAL;
+    p.row[i] = rows_host[i];
+    p.first[i] = (len_host[i] + page_size - 1) / page_size;
+    want += (new_len_host[i] + page_size - 1) / page_size - p.first[i];
+    if (want > INT32_MAX) return WPATTN_EUNSUPPORTED;
+    p.start[i + 1] = static_cast<int>(want);
+  }
+  if (want == 0) return WPATTN_OK;
+  DeviceInfo* dev = nullptr;
+  const int rc = device_info(&dev);
+  if (rc != WPATTN_OK) return rc;
+  p.table = block_table; p.refs = refs;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.n = n;
+  extend_kernel<<<1, kScanThreads, 0, static_cast<cudaStream_t>(cuda_stream)>>>(p);
+  return launched();
+}
+
+int wpattn_pages_compact(void* const* pools_host, int32_t n_pools, int32_t num_pages, int64_t page_bytes,
+                         int32_t* block_table, int64_t entries, int32_t* refs, int32_t* live,
+                         void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  CompactParams p;
+  int rc = set_pools(&p.pools, pools_host, n_pools, page_bytes);
+  if (rc != WPATTN_OK) return rc;
+  if (num_pages <= 0 || entries < 0 || (entries > 0 && !block_table) || !refs || !aligned4(block_table) ||
+      !aligned4(refs) || !aligned4(live))
+    return WPATTN_EINVAL;
+  if (!workspace || workspace_bytes < wpattn_pages_workspace_size(num_pages)) return WPATTN_EWORKSPACE;
+  if (!aligned16(workspace)) return WPATTN_EINVAL;
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  compact_plan_kernel<<<1, kScanThreads, 0, st>>>(refs, num_pages, ws, live);
+  if ((rc = launched()) != WPATTN_OK) return rc;
+  p.table = block_table; p.refs = refs; p.ws = ws; p.num_pages = num_pages;
+  p.entries = entries; p.page_bytes = page_bytes;
+  compact_kernel<<<std::min(num_pages, dev->num_sms * 8), 256, 0, st>>>(p);
+  return launched();
+}
+
+}  // extern "C"
