@@ -108,6 +108,192 @@ int64_t sum_lengths(const int32_t* len, int32_t B) {
   return sum <= INT32_MAX ? sum : -1;
 }
 
+// ------------------------------------------------------------ prefill_paged: plan and launch
+// Which CTAs run a call: sequences in order, each with the parts its row
+// blocks' key ranges are cut into; those with several parts come first.
+struct PagedPlan {
+  int n = 0, ctas = 0, split_ctas = 0;
+  uint16_t seq[kPagedMaxB], parts[kPagedMaxB];
+  int item0[kPagedMaxB + 1];
+  size_t bytes(int D) const { return static_cast<size_t>(split_ctas) * 256 * (D + 1) * sizeof(float); }
+};
+
+// Time of `count[i]` CTAs of cost[i] each, in that order, on `slots` SMs that each
+// take the next CTA when free.  SMs that are free at the same time are kept
+// together, so the work is in the number of distinct times.
+float wave_time(const int* count, const float* cost, int n, int slots) {
+  struct Level { float t; int k; };
+  Level lv[64];
+  int m = 1;
+  lv[0] = Level{0.f, slots};
+  float rest = 0.f;                       // work beyond the bookkeeping's bound, spread evenly
+  int turns = 0;
+  for (int i = 0; i < n; ++i) {
+    int left = count[i];
+    while (left > 0) {
+      if (++turns > 400 || m >= 63) { rest += left * cost[i] / slots; break; }
+      const int k = std::min(left, lv[0].k);
+      left -= k;
+      const float t = lv[0].t + cost[i];
+      if ((lv[0].k -= k) == 0) { --m; std::copy(lv + 1, lv + 1 + m, lv); }
+      int at = m;
+      while (at > 0 && lv[at - 1].t > t) --at;
+      if (at > 0 && lv[at - 1].t == t) { lv[at - 1].k += k; continue; }
+      std::copy_backward(lv + at, lv + m, lv + m + 1);
+      lv[at] = Level{t, k};
+      ++m;
+    }
+  }
+  return lv[m - 1].t + rest;
+}
+
+// Costs are in steps of a two-tile row block (a key tile for both: 1.7 us at D =
+// 128).  A one-tile block's step costs kDupStep of one, a CTA's start and end
+// kCtaSteps, the merge pass kMergeSteps.  The length of a part is the one
+// whose grid these say is done first, out of those that make about 1 .. 12
+// waves of the whole work, and no split at all.
+constexpr float kDupStep = 0.6f, kCtaSteps = 2.5f, kMergeSteps = 2.f;
+constexpr int kMinPartTiles = 3, kMaxParts = 64;
+
+bool plan_paged(const int32_t* q_len, const int32_t* kv_len, int B, int G, int Hkv, int D, int num_sms,
+                PagedPlan* out) {
+  (void)D;
+  const int tile_tokens = 128 / G;
+  struct Work { int b, blocks, nkt; float step; };
+  Work w[kPagedMaxB];
+  int n = 0, longest = 0;
+  double total = 0;
+  for (int b = 0; b < B; ++b) {
+    if (q_len[b] == 0) continue;
+    const int tiles = (q_len[b] + tile_tokens - 1) / tile_tokens;
+    w[n] = Work{b, (tiles + 1) / 2, (kv_len[b] + 127) / 128, tiles > 1 ? 1.f : kDupStep};
+    total += static_cast<double>(w[n].blocks) * Hkv * w[n].nkt * w[n].step;
+    longest = std::max(longest, w[n].nkt);
+    ++n;
+  }
+  // longest rows first
+  std::sort(w, w + n, [](const Work& a, const Work& b) {
+    return a.nkt * a.step != b.nkt * b.step ? a.nkt * a.step > b.nkt * b.step : a.b < b.b;
+  });
+  auto parts_of = [&](const Work& x, int len) {   // parts of at most `len` step costs
+    const int tiles = std::max(kMinPartTiles, static_cast<int>(len / x.step));
+    return std::min(kMaxParts, std::max(1, (x.nkt + tiles - 1) / tiles));
+  };
+  int count[kPagedMaxB];
+  float cost[kPagedMaxB];
+  int best_len = INT32_MAX;
+  float best = 0;
+  for (int k = 0; k <= 12; ++k) {
+    const int len = k == 0 ? INT32_MAX / 2 : static_cast<int>(total / (static_cast<double>(num_sms) * k)) + 1;
+    if (k > 0 && len >= longest) continue;        // nothing would be split
+    if (k > 0 && len < kMinPartTiles) break;
+    int m = 0;
+    bool split = false;
+    for (int i = 0; i < n; ++i) {
+      const int parts = parts_of(w[i], len);
+      const float c = (w[i].nkt + parts - 1) / parts * w[i].step + kCtaSteps;
+      const int64_t ctas = int64_t(w[i].blocks) * Hkv * parts;
+      split |= parts > 1;
+      if (ctas > INT32_MAX / 2) return false;
+      if (m > 0 && cost[m - 1] == c && count[m - 1] < INT32_MAX / 2) count[m - 1] += static_cast<int>(ctas);
+      else { cost[m] = c; count[m++] = static_cast<int>(ctas); }
+    }
+    const float t = wave_time(count, cost, m, num_sms) + (split ? kMergeSteps : 0.f);
+    if (k == 0 || t < best) { best = t; best_len = len; }
+  }
+  // split sequences first: only their CTAs have room in the workspace
+  int64_t ctas = 0;
+  out->n = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int i = 0; i < n; ++i) {
+      const int parts = parts_of(w[i], best_len);
+      if ((parts > 1) != (pass == 0)) continue;
+      out->item0[out->n] = static_cast<int>(ctas);
+      out->seq[out->n] = static_cast<uint16_t>(w[i].b);
+      out->parts[out->n++] = static_cast<uint16_t>(parts);
+      ctas += int64_t(w[i].blocks) * Hkv * parts;
+      if (ctas > INT32_MAX) return false;
+    }
+    if (pass == 0) out->split_ctas = static_cast<int>(ctas);
+  }
+  out->item0[out->n] = out->ctas = static_cast<int>(ctas);
+  return true;
+}
+
+struct PagedCall {
+  DeviceInfo* dev;
+  PagedPlan plan;
+  const WindowPlan* window;
+  const void *q, *k, *v;
+  void *out, *workspace;
+  float* lse;
+  const int32_t *block_table, *q_len, *kv_len;
+  int num_pages, page_size, max_pages, B, Hq, Hkv;
+  float scale;
+  cudaStream_t st;
+};
+
+template <int D, bool G8, int MAXB>
+int launch_paged(const PagedCall& c) {
+  using L = PagedSmem<D>;
+  PrefillPagedParams<MAXB> p;
+  std::memset(&p, 0, sizeof p);
+  p.q = static_cast<const uint16_t*>(c.q);
+  p.block_table = c.block_table;
+  p.out = static_cast<uint16_t*>(c.out);
+  p.lse = c.lse;
+  p.part_o = static_cast<float*>(c.workspace);
+  p.part_l = p.part_o + static_cast<size_t>(c.plan.split_ctas) * 256 * D;
+  p.B = c.plan.n; p.Hq = c.Hq; p.Hkv = c.Hkv; p.G = c.Hq / c.Hkv;
+  p.num_pages = c.num_pages; p.page_size = c.page_size; p.max_pages = c.max_pages;
+  p.unit = std::min(128, c.page_size & -c.page_size);
+  p.tile_tokens = 128 / p.G;
+  p.scale_log2 = c.scale * 1.44269504088896340736f;
+  for (int i = 0; i < 64; ++i)
+    p.T[i] = c.window->T[i] > INT32_MAX ? INT32_MAX : static_cast<int>(c.window->T[i]);
+  std::copy(c.plan.item0, c.plan.item0 + c.plan.n + 1, p.item0);
+  std::copy(c.plan.seq, c.plan.seq + c.plan.n, p.seq);
+  std::copy(c.plan.parts, c.plan.parts + c.plan.n, p.parts);
+  for (int b = 0; b < c.B; ++b) {
+    p.q_start[b + 1] = p.q_start[b] + c.q_len[b];
+    p.kv_len[b] = c.kv_len[b];
+  }
+  // pools as groups of 8 keys: (64 dims, 8 keys, panels of every head, groups)
+  const cuuint64_t row = static_cast<cuuint64_t>(c.Hkv) * D * 2;
+  const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(c.Hkv) * (D / 64),
+                              static_cast<cuuint64_t>(c.num_pages) * c.page_size / 8};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {64, 8, D / 64, static_cast<cuuint32_t>(p.unit / 8)}, estr[4] = {1, 1, 1, 1};
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return WPATTN_ECUDA;
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i)
+    if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i ? c.v : c.k), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return WPATTN_ECUDA;
+  const auto kernel = prefill_paged_kernel<D, G8, MAXB>;
+  static std::atomic<bool> attr_set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return WPATTN_ECUDA;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) != cudaSuccess)
+      return WPATTN_ECUDA;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  kernel<<<c.plan.ctas, 384, L::ALLOC, c.st>>>(maps[0], maps[1], p);
+  const int rc = launched();
+  if (rc != WPATTN_OK || c.plan.split_ctas == 0) return rc;
+  prefill_paged_merge_kernel<D, MAXB><<<dim3(c.plan.split_ctas, D / 32), 256, 0, c.st>>>(p);
+  return launched();
+}
+
+template <int D, bool G8>
+int run_paged(const PagedCall& c) {
+  // a launch copies its parameters: 17 KB for 1024 sequences, 1.5 KB for 64
+  return c.B <= 64 ? launch_paged<D, G8, 64>(c) : launch_paged<D, G8, kPagedMaxB>(c);
+}
+
 }  // namespace
 }  // namespace wpattn
 
@@ -179,8 +365,17 @@ int wpattn_append_paged(const void* k, int64_t k_stride, const void* v, int64_t 
 
 size_t wpattn_prefill_paged_workspace_size(const wpattn_window* w, const int32_t* q_len_host,
                                            const int32_t* kv_len_host, int32_t B, int32_t Hq, int32_t Hkv) {
-  (void)w; (void)q_len_host; (void)kv_len_host; (void)B; (void)Hq; (void)Hkv;
-  return 0;
+  WindowPlan plan;
+  if (make_window_plan(w, &plan) != WPATTN_OK || (plan.D != 64 && plan.D != 128)) return 0;
+  if (B <= 0 || B > kPagedMaxB || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 128 || !q_len_host || !kv_len_host)
+    return 0;
+  if (sum_lengths(q_len_host, B) < 0) return 0;
+  for (int b = 0; b < B; ++b)
+    if (kv_len_host[b] < 0 || kv_len_host[b] > (1 << 30)) return 0;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev) != WPATTN_OK) return 0;
+  PagedPlan pp;
+  return plan_paged(q_len_host, kv_len_host, B, Hq / Hkv, Hkv, plan.D, dev->num_sms, &pp) ? pp.bytes(plan.D) : 0;
 }
 
 int wpattn_prefill_paged(const wpattn_window* w, const void* q, const void* k_pages, const void* v_pages,
@@ -203,35 +398,27 @@ int wpattn_prefill_paged(const wpattn_window* w, const void* q, const void* k_pa
   for (int b = 0; b < B; ++b)
     if (kv_len_host[b] < 0 || kv_len_host[b] > cap) return WPATTN_EINVAL;
   if (tokens == 0) return WPATTN_OK;
-  if (!q || !out || !k_pages || !v_pages || !block_table || !aligned4(block_table)) return WPATTN_EINVAL;
+  if (!q || !out || !k_pages || !v_pages || !block_table || !aligned4(block_table) || !aligned4(lse))
+    return WPATTN_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(k_pages) || !aligned16(v_pages)) return WPATTN_EINVAL;
   if (cap > (int64_t(1) << 30) || int64_t(num_pages) * page_size >= (int64_t(1) << 31)) return WPATTN_EUNSUPPORTED;
-  DeviceInfo* dev = nullptr;
-  if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
-  (void)workspace; (void)workspace_bytes;
-  PrefillPagedParams p;
-  std::memset(&p, 0, sizeof p);
-  p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k_pages);
-  p.v = static_cast<const uint16_t*>(v_pages);
-  p.block_table = block_table;
-  p.out = static_cast<uint16_t*>(out);
-  p.lse = lse;
-  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
-  p.num_pages = num_pages; p.page_size = page_size; p.max_pages = max_pages_per_seq;
-  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(plan.D));
-  p.scale_log2 = scale * 1.44269504088896340736f;
-  for (int i = 0; i < 64; ++i) p.T[i] = plan.T[i] > INT32_MAX ? INT32_MAX : static_cast<int>(plan.T[i]);
-  for (int b = 0; b < B; ++b) {
-    p.q_start[b + 1] = p.q_start[b] + q_len_host[b];
-    p.kv_len[b] = kv_len_host[b];
+  PagedCall c;
+  if ((rc = device_info(&c.dev)) != WPATTN_OK) return rc;
+  if (!plan_paged(q_len_host, kv_len_host, B, Hq / Hkv, Hkv, plan.D, c.dev->num_sms, &c.plan))
+    return WPATTN_EUNSUPPORTED;
+  if (c.plan.split_ctas > 0) {
+    if (!workspace || workspace_bytes < c.plan.bytes(plan.D)) return WPATTN_EWORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return WPATTN_EINVAL;
   }
-  const int64_t blocks = (tokens * Hq + 7) / 8;
-  if (blocks > INT32_MAX) return WPATTN_EUNSUPPORTED;
-  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (plan.D == 64) prefill_paged_kernel<64><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
-  else prefill_paged_kernel<128><<<static_cast<unsigned>(blocks), 256, 0, st>>>(p);
-  return launched();
+  c.window = &plan;
+  c.q = q; c.k = k_pages; c.v = v_pages; c.out = out; c.lse = lse; c.workspace = workspace;
+  c.block_table = block_table; c.q_len = q_len_host; c.kv_len = kv_len_host;
+  c.num_pages = num_pages; c.page_size = page_size; c.max_pages = max_pages_per_seq;
+  c.B = B; c.Hq = Hq; c.Hkv = Hkv;
+  c.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(plan.D));
+  c.st = static_cast<cudaStream_t>(cuda_stream);
+  if (plan.D == 64) return plan.g == 8 ? run_paged<64, true>(c) : run_paged<64, false>(c);
+  return plan.g == 8 ? run_paged<128, true>(c) : run_paged<128, false>(c);
 }
 
 int wpattn_pages_copy(void* const* pools_host, int32_t n_pools, int32_t num_pages, int64_t page_bytes,

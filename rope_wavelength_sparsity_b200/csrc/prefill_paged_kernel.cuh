@@ -1,43 +1,116 @@
-// Windowed causal attention of a ragged batch of chunks over a paged KV cache.
+// Windowed causal attention of a ragged batch of chunks over a paged KV cache
+// (TMA + tcgen05 + TMEM).
 //
 // "ATFlash: Per-RoPE-Wavelength Attention Windows", Abstract: the window is a
 // slice of the query-key contraction axis and the online softmax is left
 // untouched.  Query t of sequence b sits at kv_len - q_len + t and attends
 // the sequence's keys 0 .. its position, found through the block table.
 //
-// One warp per (token, query head): a lane scores one key of a block of 32
-// over the pairs kept at its distance, then the lanes share the block's
-// weights and accumulate D / 32 output dims each.
+// Rows.  A tile's 128 rows are (token, head of one kv group) pairs, token
+// by token: 128 / G tokens (rounded down) of all G query heads that read one
+// kv head.  A cached key is thus read once for the whole group even when a
+// sequence brings a single token, and a tile spans few positions, so fewer
+// pairs are kept at some but not all of a key tile's distances.
+//
+// One CTA owns a row block (two row tiles that share every key tile) of one
+// kv head of one sequence, over all or a part of the keys.  A row block with
+// one tile runs it twice: its key tiles alternate between the two softmax
+// groups (`dup`), which merge their halves at the end, so that one group's
+// softmax overlaps the other's products there too.  Parts of a key range leave
+// normalised fp32 results, merged by prefill_paged_merge_kernel.
+//
+// Warp roles (12 warps) as in the contiguous prefill:
+//   warps 0-3, 4-7  softmax of tile 0 / 1: row r is TMEM lane r.  They bring Q
+//              in, correct the pairs kept at some but not all distances of a
+//              tile, mask, run the online softmax, write P (bf16) over S.
+//   warp 8     TMA producer: lane u copies unit u of a key tile (R keys of one
+//              page, R = the largest power of two that divides the page, up
+//              to 128), K and V by one copy each.
+//   warp 9     MMA issuer (one lane); owns the TMEM allocation.
+//   warp 10    zeroes the V rows behind the sequence's last key, which may
+//              hold anything (0 * NaN would reach every row's output).
+//
+// Shared-memory layouts.  K and V tiles are groups of 8 keys, each D / 64
+// panels of 8 rows x 128 bytes, 128-byte swizzled: the layout one 4-D copy
+// (64 dims, 8 keys, panels, groups) leaves, whatever the page size.  16-byte
+// wide boxes, which would let a contraction step pair any two 8-dim columns,
+// move a 32 KB tile in 1.17 us against 0.69 us at 128 bytes (0.31 us from
+// L2), as long as the tile's whole arithmetic; so a step takes 16 dims of one
+// half, and a unit of 16 pairs is two steps.  Q is no-swizzle K-major:
+// 16-byte columns of 128 rows, 2 KB apart.
+//
+// TMEM columns: S_t / P_t at [128 t, 128 t + 128), O_t at 256 + t D.
 #pragma once
 
 #include "device_util.cuh"
+#include "prefill_kernel.cuh"
 
 namespace wpattn {
 
 constexpr int kPagedMaxB = 1024;
 
+template <int MAXB>
 struct PrefillPagedParams {
   const uint16_t* q;        // [T, Hq, D]
-  const uint16_t* k;        // [num_pages, page_size, Hkv, D]
-  const uint16_t* v;
   const int32_t* block_table;  // [B, max_pages]
   uint16_t* out;            // [T, Hq, D]
   float* lse;               // [T, Hq] or null
+  // parts: row r of CTA c at part_l[c * 256 + r], its dims 8 e .. 8 e + 7 at
+  // part_o[((c * D / 8 + e) * 256 + r) * 8]
+  float* part_o;
+  float* part_l;            // log2-sum-exp, -inf: no key
   int B, Hq, Hkv, G, num_pages, page_size, max_pages;
+  int unit;                 // keys per copy
+  int tile_tokens;          // 128 / G
   float scale_log2;         // softmax scale * log2(e)
   int T[64];                // per-pair thresholds, clamped to int32
-  int q_start[kPagedMaxB + 1];  // first row of each sequence in q
-  int kv_len[kPagedMaxB];
+  // sequences in the order of the grid: CTA c belongs to the i-th when item0[i] <= c < item0[i + 1]
+  int item0[MAXB + 1];
+  uint16_t seq[MAXB];
+  uint16_t parts[MAXB];     // key ranges of each of its row blocks
+  int q_start[MAXB + 1];    // by sequence: first row in q
+  int kv_len[MAXB];
 };
 
-// The sequence whose rows cover `token` (start: B + 1 non-decreasing offsets, token < start[B]).
-__device__ __forceinline__ int find_sequence(const int* start, int B, int token) {
-  int lo = 0, hi = B - 1;
+// The i with start[i] <= at < start[i + 1] (start: n + 1 non-decreasing offsets, at < start[n]).
+__device__ __forceinline__ int find_sequence(const int* start, int n, int at) {
+  int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= token) lo = mid; else hi = mid - 1;
+    if (start[mid] <= at) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// What CTA c works on.
+struct PagedItem {
+  int b, kvh, rb, part, parts;
+  int q_len, kv_len, row0;  // row0: the sequence's first row in q
+  int tok[2], ntok[2];      // first token and tokens of each row tile
+  bool dup;
+};
+
+template <int MAXB>
+__device__ __forceinline__ PagedItem paged_item(const PrefillPagedParams<MAXB>& p, int c) {
+  PagedItem it;
+  const int i = find_sequence(p.item0, p.B, c);
+  const int local = c - p.item0[i];
+  it.b = p.seq[i];
+  it.parts = p.parts[i];
+  it.row0 = p.q_start[it.b];
+  it.q_len = p.q_start[it.b + 1] - it.row0;
+  it.kv_len = p.kv_len[it.b];
+  const int tiles = (it.q_len + p.tile_tokens - 1) / p.tile_tokens, blocks = (tiles + 1) >> 1;
+  it.rb = blocks - 1 - local % blocks;   // longest rows first
+  it.kvh = local / blocks % p.Hkv;
+  it.part = local / blocks / p.Hkv;
+  it.dup = 2 * it.rb + 1 >= tiles;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.tok[t] = (2 * it.rb + (it.dup ? 0 : t)) * p.tile_tokens;
+    it.ntok[t] = min(p.tile_tokens, it.q_len - it.tok[t]);
+  }
+  return it;
 }
 
 // A block-table entry; one outside the pool is recorded and page 0 stands in for it.
@@ -50,57 +123,718 @@ __device__ __forceinline__ int checked_page(int pg, int num_pages) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(256)
-prefill_paged_kernel(const __grid_constant__ PrefillPagedParams p) {
-  constexpr int P = D / 2, E = D / 32;
+struct PagedSmem {
+  static constexpr int NSK = D == 64 ? 4 : 2;        // K ring; one more when `dup` leaves tile 1's Q free
+  static constexpr int NSV = NSK;
+  static constexpr int TILE = 128 * D * 2;           // a tile of K, V or Q
+  static constexpr int GROUP = 8 * D * 2;            // 8 keys
+  static constexpr int COL = 128 * 16;               // 16-byte column of Q
+  static constexpr int OFF_V = 0;
+  static constexpr int OFF_K = OFF_V + NSV * TILE;
+  static constexpr int OFF_Q1 = OFF_K + NSK * TILE;
+  static constexpr int OFF_Q0 = OFF_Q1 + TILE;
+  static constexpr int OFF_QM = OFF_Q0 + TILE;       // per tile: Q's first unit with its left-out pairs zeroed
+  static constexpr int OFF_SCR = OFF_QM + 2 * 4 * COL;   // per warp [32 rows][16 keys] fp32
+  static constexpr int OFF_T = OFF_SCR + 8 * 2048;
+  static constexpr int OFF_BAR = OFF_T + 64 * 4;
+  // k_full, k_empty [NSK + 1], v_full, v_empty [NSV], s_full, p_full, o_final, q_ready [2], v_fix
+  static constexpr int NBAR = 2 * (NSK + 1) + 2 * NSV + 9;
+  static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+  static constexpr int ALLOC = OFF_TMEM + 16;
+};
+static_assert(PagedSmem<128>::ALLOC <= 232448 && PagedSmem<64>::ALLOC <= 232448, "shared memory of one CTA");
+
+template <int D, bool G8, int MAXB>
+__global__ void __launch_bounds__(384, 1)
+prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ PrefillPagedParams<MAXB> p) {
+  using L = PagedSmem<D>;
+  constexpr int P = D / 2;
+  constexpr int NSV = L::NSV, TILE = L::TILE, COL = L::COL;
+  constexpr int W_PROD = 8, W_MMA = 9, W_FIX = 10;
+  constexpr uint32_t TMEM_O = 256;
   constexpr uint32_t FULL = 0xffffffffu;
-  __shared__ float sq[8][D];
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar = sbase + L::OFF_BAR;
+  auto k_full = [&](int s) { return bar + 8 * s; };
+  auto k_empty = [&](int s) { return bar + 8 * (L::NSK + 1 + s); };
+  auto v_full = [&](int s) { return bar + 8 * (2 * L::NSK + 2 + s); };
+  auto v_empty = [&](int s) { return bar + 8 * (2 * L::NSK + 2 + NSV + s); };
+  constexpr int B0 = 2 * L::NSK + 2 + 2 * NSV;
+  auto s_full = [&](int t) { return bar + 8 * (B0 + t); };
+  auto p_full = [&](int t) { return bar + 8 * (B0 + 2 + t); };
+  auto o_final = [&](int t) { return bar + 8 * (B0 + 4 + t); };
+  auto q_ready = [&](int t) { return bar + 8 * (B0 + 6 + t); };
+  const uint32_t v_fix = bar + 8 * (B0 + 8);
+  int* sT = reinterpret_cast<int*>(smem + L::OFF_T);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM);
+
+  // the swizzled tiles need a 1024-byte aligned shared window
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) record_status(2 /* WPATTN_EUNSUPPORTED */);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp;
-  if (row >= static_cast<int64_t>(p.q_start[p.B]) * p.Hq) return;
-  const int token = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
-  const int b = find_sequence(p.q_start, p.B, token);
-  const int kvh = h / p.G;
-  const int pos = p.kv_len[b] - p.q_start[b + 1] + token;   // kv_len - q_len + t
-  for (int e = lane; e < D; e += 32) sq[warp][e] = bf16lo_to_f32(p.q[row * D + e]);
+  const PagedItem it = paged_item(p, blockIdx.x);
+  const bool dup = it.dup;
+  const int nkt = (it.kv_len + 127) >> 7;
+  const int per = (nkt + it.parts - 1) / it.parts;
+  const int kt_lo = it.part * per, kt_hi = min(kt_lo + per, nkt) - 1;
+  const int pos0 = it.kv_len - it.q_len;              // the chunk's first position
+  auto q_first = [&](int t) { return pos0 + it.tok[t]; };
+  // key tiles of row tile t: kt_lo .. kt_last[t], walked downwards; none: kt_lo - 1
+  int kt_last[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int i_max = q_first(t) + it.ntok[t] - 1;
+    kt_last[t] = i_max < 0 ? kt_lo - 1 : max(min(i_max >> 7, kt_hi), kt_lo - 1);
+  }
+  const int top = max(kt_last[0], kt_last[1]);
+  const int steps = top - kt_lo + 1;                  // step j is key tile top - j
+  auto attends = [&](int t, int j) { return dup ? (j & 1) == t : top - j <= kt_last[t]; };
+  const int nsk = L::NSK + (dup ? 1 : 0);
+  const bool tail = steps > 0 && top == nkt - 1 && (it.kv_len & 127) != 0;
+
+  // First pair kept somewhere in a tile (only moves forward along the walk).
+  auto advance_plo = [&](int t, int kt, int& plo) {
+    const int dlo = q_first(t) - (128 * kt + 127);
+    while (plo < P && sT[plo] < dlo) ++plo;
+  };
+  // Split pair: pairs plo .. ps - 1 are left out of the contraction and added
+  // back where they are kept; pairs ps .. P - 1 are contracted and subtracted
+  // where they are pruned.  At the pair first kept 32 past the tile's centre
+  // distance both sets are small (thresholds grow geometrically).
+  auto split_pair = [&](int t, int kt, int plo, int& psr) -> int {
+    if (plo >= P) return plo;
+    const int dc = max(q_first(t) - 128 * kt + (p.tile_tokens >> 1) - 64, 0);
+    while (psr < P && sT[psr] < dc + 32) ++psr;
+    return min(max(psr, plo), P - (G8 ? 8 : 1));
+  };
+
+  if (threadIdx.x < 64) sT[threadIdx.x] = p.T[threadIdx.x];
+  if (threadIdx.x == 0) {
+    for (int s = 0; s <= L::NSK; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), dup ? 5 : 9);   // MMA commit + the softmax warps that attend the stage
+    }
+    for (int s = 0; s < NSV; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);
+      mbar_init(o_final(t), 1);
+      mbar_init(q_ready(t), 4);
+    }
+    mbar_init(v_fix, 1);
+    fence_barrier_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= W_PROD) {
+    regs_decrease<56>();
+    if (warp == W_PROD) {
+      // ---------------------------------------------------------- producer
+      const int R = p.unit, units = 128 / R;
+      const int32_t* table = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
+      // this lane's unit of key tile kt: its 8-key group in the pool, -1: no key
+      auto fetch = [&](int kt) -> int {
+        const int key = 128 * kt + lane * R;
+        if (kt < kt_lo || lane >= units || key >= it.kv_len) return -1;
+        const int pg = checked_page(__ldg(table + key / p.page_size), p.num_pages);
+        return (pg * p.page_size + key % p.page_size) >> 3;
+      };
+      if (lane == 0) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+      }
+      int next = fetch(top), nk = 0, nv = 0;   // nk, nv: tiles whose copies were issued
+      bool ok = true;
+      int sk = 0, pk = 0;
+      for (int j = 0; j < steps; ++j) {
+        const int at = next, kt = top - j, sv = j % NSV;
+        const uint32_t bytes = __popc(__ballot_sync(FULL, at >= 0)) * R * D * 2;
+        if (j >= nsk && !__all_sync(FULL, mbar_wait(k_empty(sk), pk ^ 1))) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(k_full(sk), bytes);
+        __syncwarp();
+        if (at >= 0)
+          tma_load_4d(sbase + L::OFF_K + sk * TILE + lane * R * D * 2, &tmK, k_full(sk), 0, 0, it.kvh * (D / 64), at);
+        nk = j + 1;
+        if (++sk == nsk) { sk = 0; pk ^= 1; }
+        next = fetch(kt - 1);
+        if (j >= NSV && !__all_sync(FULL, mbar_wait(v_empty(sv), ((j / NSV) & 1) ^ 1))) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(v_full(sv), bytes);
+        __syncwarp();
+        if (at >= 0)
+          tma_load_4d(sbase + L::OFF_V + sv * TILE + lane * R * D * 2, &tmV, v_full(sv), 0, 0, it.kvh * (D / 64), at);
+        nv = j + 1;
+      }
+      if (!ok) {
+        // A wait ran out: wait (bounded) for the copies that may still be landing
+        for (int j = max(0, nk - nsk); j < nk; ++j) (void)mbar_wait(k_full(j % nsk), (j / nsk) & 1);
+        for (int j = max(0, nv - NSV); j < nv; ++j) (void)mbar_wait(v_full(j % NSV), (j / NSV) & 1);
+      }
+    } else if (warp == W_MMA) {
+      // -------------------------------------------------------- MMA issuer
+      if (lane == 0 && steps > 0) {
+        constexpr uint32_t idesc_qk = make_idesc_bf16(128, 128, 0, 0);
+        constexpr uint32_t idesc_pv = make_idesc_bf16(128, D, 0, 1);
+        const uint64_t qdesc = make_sdesc(sbase + L::OFF_Q0, COL, 128, 0);
+        const uint64_t q1desc = make_sdesc(sbase + L::OFF_Q1, COL, 128, 0);
+        const uint64_t qmdesc = make_sdesc(sbase + L::OFF_QM, COL, 128, 0);
+        const uint64_t kdesc = make_sdesc(sbase + L::OFF_K, 16, L::GROUP, 2);
+        const uint64_t vdesc = make_sdesc(sbase + L::OFF_V, 1024, L::GROUP, 2);
+        const int ahead = dup ? 2 : 1;         // a tile's next QK follows its PV
+        int cnt[2] = {0, 0}, plo[2] = {0, 0}, psr[2] = {0, 0};
+        bool q_seen[2] = {false, false};
+        bool ok = true;
+        int sk = 0, pk = 0;                    // ring position of the next QK's key tile
+        auto plan_qk = [&](int t, int j) -> int {
+          advance_plo(t, top - j, plo[t]);
+          return split_pair(t, top - j, plo[t], psr[t]);
+        };
+        auto issue_qk = [&](int t, int ps) -> bool {
+          if (!q_seen[t]) {
+            if (!mbar_wait(q_ready(t), 0)) return false;
+            q_seen[t] = true;
+            tc_fence_after();
+          }
+          const uint64_t kb = kdesc + static_cast<uint64_t>((sk * TILE) >> 4);
+          const uint64_t qb = (dup || t == 0) ? qdesc : q1desc;
+          const int u0 = ps >> 4;
+          for (int u = u0; u < P / 16; ++u) {
+            const bool masked = u == u0 && (ps & 15);
+            const uint64_t a = masked ? qmdesc + static_cast<uint64_t>((t * 4 * COL) >> 4)
+                                      : qb + static_cast<uint64_t>((2 * u * COL) >> 4);
+            const uint64_t a2 = a + static_cast<uint64_t>(((masked ? 2 : D / 16) * COL) >> 4);
+            // the unit's second halves: the next 64-dim panel (D = 128), or 64 bytes on (D = 64)
+            const uint64_t b = kb + static_cast<uint64_t>((u * 32) >> 4);
+            const uint64_t b2 = b + static_cast<uint64_t>((D == 128 ? 1024 : 64) >> 4);
+            umma_ss(tmem + t * 128, a, b, idesc_qk, u > u0 ? 1u : 0u);
+            umma_ss(tmem + t * 128, a2, b2, idesc_qk, 1u);
+          }
+          umma_commit(s_full(t));
+          return true;
+        };
+        for (int j = 0; ok && j < min(ahead, steps); ++j) {
+          ok = mbar_wait(k_full(sk), pk);
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (ok && attends(t, j)) ok = issue_qk(t, plan_qk(t, j));
+          if (!ok) break;
+          umma_commit(k_empty(sk));
+          if (++sk == nsk) { sk = 0; pk ^= 1; }
+        }
+        for (int j = 0; ok && j < steps; ++j) {
+          const int jn = j + ahead, sv = j % NSV;
+          const bool next = jn < steps;
+          if (!mbar_wait(v_full(sv), (j / NSV) & 1)) { ok = false; break; }
+          if (tail && j == 0 && !mbar_wait(v_fix, 0)) { ok = false; break; }
+          const uint64_t vb = vdesc + static_cast<uint64_t>((sv * TILE) >> 4);
+          bool k_seen = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const bool do_qk = ok && next && attends(t, jn);
+            const int ps = do_qk ? plan_qk(t, jn) : 0;
+            if (ok && attends(t, j)) {
+              if (!mbar_wait_handoff(p_full(t), cnt[t] & 1)) ok = false;
+              if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  umma_ts(tmem + TMEM_O + t * D, tmem + t * 128 + ks * 8,
+                              vb + static_cast<uint64_t>((ks * 2 * L::GROUP) >> 4), idesc_pv,
+                              (cnt[t] > 0 || ks > 0) ? 1u : 0u);
+                ++cnt[t];
+              }
+            }
+            if (ok && do_qk) {
+              if (!k_seen) {
+                ok = mbar_wait_handoff(k_full(sk), pk);
+                k_seen = true;
+              }
+              ok = ok && issue_qk(t, ps);
+            }
+          }
+          if (!ok) break;
+          umma_commit(v_empty(sv));
+          if (next) {
+            umma_commit(k_empty(sk));
+            if (++sk == nsk) { sk = 0; pk ^= 1; }
+          }
+        }
+        // every MMA issued so far has completed once these arrive
+        for (int t = 0; t < 2; ++t) umma_commit(o_final(t));
+        if (!ok) mbar_wait(o_final(0), 0);
+      }
+    } else if (warp == W_FIX && tail) {
+      if (__all_sync(FULL, mbar_wait(v_full(0), 0))) {
+        constexpr int ROW_CHUNKS = D / 8;
+        for (int i = (it.kv_len & 127) * ROW_CHUNKS + lane; i < 128 * ROW_CHUNKS; i += 32) {
+          const int row = i / ROW_CHUNKS, c = i % ROW_CHUNKS;
+          *reinterpret_cast<uint4*>(smem + L::OFF_V + (row >> 3) * L::GROUP + (c >> 3) * 1024 + (row & 7) * 128 +
+                                    (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_fix);
+      }
+    }
+  } else {
+    regs_increase<224>();
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2;
+    const int wq = warp & 3;
+    const int r = wq * 32 + lane;              // row of the tile = TMEM lane
+    const int tok = r / p.G;
+    const bool row_ok = r < p.tile_tokens * p.G && tok < it.ntok[t];
+    const int i_pos = q_first(t) + min(tok, it.ntok[t] - 1);   // rows without a token walk with the last
+    const size_t qrow = (static_cast<size_t>(it.row0) + it.tok[t] + (row_ok ? tok : 0)) * p.Hq +
+                        static_cast<size_t>(it.kvh) * p.G + (row_ok ? r % p.G : 0);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tS = lane_base + t * 128;
+    const uint32_t tO = lane_base + TMEM_O + t * D;
+    uint8_t* smem_q = smem + ((dup || t == 0) ? L::OFF_Q0 : L::OFF_Q1);
+    uint8_t* smem_qm = smem + L::OFF_QM + t * 4 * COL;
+    const int my_last = kt_last[t];
+    float m_ref = -INFINITY;   // exponent reference of O and l (log2 units)
+    float l_run = 0.f;
+    int cnt = 0;
+    bool ok = true;
+
+    if (steps > 0 && !(dup && t == 1)) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + qrow * D);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<uint4*>(smem_q + c * COL + r * 16) = row_ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");   // dup: group 1 reads group 0's rows
+
+    // Copy of Q's unit of 16 pairs that starts the contraction for split pair
+    // ps, its pairs below ps zeroed.  The split pair only moves forward and
+    // mostly stays put, so an unchanged copy is kept.
+    int qm_ps = -1;
+    auto write_masked_q = [&](int ps) {
+      const int rz = ps & 15;
+      if (rz == 0 || ps >= P || ps == qm_ps) return;
+      qm_ps = ps;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int first = 8 * (c & 1);         // the column's first pair within the unit
+        uint4 x = *reinterpret_cast<const uint4*>(smem_q + (2 * (ps >> 4) + (c & 1) + (c >> 1) * (D / 16)) * COL + r * 16);
+        const int z = rz - first;              // pairs zeroed in this column
+        x.x &= (z > 0 ? 0u : 0xFFFFu) | (z > 1 ? 0u : 0xFFFF0000u);
+        x.y &= (z > 2 ? 0u : 0xFFFFu) | (z > 3 ? 0u : 0xFFFF0000u);
+        x.z &= (z > 4 ? 0u : 0xFFFFu) | (z > 5 ? 0u : 0xFFFF0000u);
+        x.w &= (z > 6 ? 0u : 0xFFFFu) | (z > 7 ? 0u : 0xFFFF0000u);
+        *reinterpret_cast<uint4*>(smem_qm + c * COL + r * 16) = x;
+      }
+      fence_proxy_async_smem();
+    };
+
+    // this tile's steps: every `stride`-th from j0 on
+    const int stride = dup ? 2 : 1;
+    const int j0 = dup ? t : top - my_last;
+    int plo_next = 0, psr = 0, ps_next = 0;
+    auto plan = [&](int j) {
+      advance_plo(t, top - j, plo_next);
+      ps_next = split_pair(t, top - j, plo_next, psr);
+    };
+    if (j0 < steps) {
+      plan(j0);
+      write_masked_q(ps_next);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_ready(t));
+
+    int sk = 0, pk = 0;
+    auto next_stage = [&]() {
+      if (++sk == nsk) { sk = 0; pk ^= 1; }
+    };
+    // key tiles that only the other row tile attends: release them
+    for (int j = 0; ok && j < min(j0, steps); ++j) {
+      if (!dup) {
+        // wait for the stage's fill, so that the arrival counts towards this phase
+        if (!__all_sync(FULL, mbar_wait(k_full(sk), pk))) { ok = false; break; }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_empty(sk));
+      }
+      next_stage();
+    }
+
+    for (int j = j0; ok && j < steps; j += stride) {
+      const int kt = top - j;
+      const int kp0 = 128 * kt;
+      const int d_row = i_pos - kp0;           // distance to the tile's first key
+      const int plo = plo_next, ps = ps_next;
+      const bool all_pruned = plo >= P;
+      const bool more = j + stride < steps;
+      if (more) plan(j + stride);
+
+      // Per-element corrections, d = d_row - c for column c of the tile:
+      // pairs plo .. ps - 1 were left out: add them where 0 <= d <= T;
+      // pairs ps .. P - 1 were contracted: subtract them where d > T.
+      const bool need_sub = !all_pruned && __any_sync(FULL, d_row > sT[ps]);
+      const bool need_add = !all_pruned && ps > plo && __any_sync(FULL, d_row >= 0 && d_row - 127 <= sT[ps - 1]);
+      const bool corr = need_sub || need_add;
+      const uint32_t kb = sbase + L::OFF_K + sk * TILE;
+      const uint32_t stage_empty = k_empty(sk);
+      // waiting for the fill first makes the release below count towards this phase
+      if (!__all_sync(FULL, mbar_wait(k_full(sk), pk))) { ok = false; break; }
+      next_stage();
+      if (dup) next_stage();
+      if (!corr) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(stage_empty);
+      }
+      if (!__all_sync(FULL, mbar_wait_handoff(s_full(t), cnt & 1))) { ok = false; break; }
+      tc_fence_after();
+      if (corr) {
+        // The products of a group of 8 pairs (or of one pair: its group's with
+        // the other pairs' Q elements zeroed) for this warp's 32 rows by
+        // warp-level MMAs, m16n8k16: A = Q rows, dims 8 grp .. then P + 8 grp
+        // .., B = K rows; a per-warp scratch turns them into one row per lane.
+        float* scr = reinterpret_cast<float*>(smem + L::OFF_SCR) + warp * 512;   // [32 rows][16 keys]
+        const int qm = lane >> 3, qi = lane & 7;
+        uint32_t afr[2][4];
+        auto load_a = [&](int grp) {           // matrix m: rows 8 (m & 1) .., half m >> 1
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            const int row_a = wq * 32 + 16 * mt + 8 * (qm & 1) + qi;
+            const int col = (qm >> 1) ? P / 8 + grp : grp;
+            ldsm_x4(smem_u32(smem_q) + col * COL + row_a * 16, afr[mt][0], afr[mt][1], afr[mt][2], afr[mt][3]);
+          }
+        };
+        // v[c] += sgn * product, for this row's columns lo .. hi of chunk cc
+        auto apply = [&](float (&v)[32], int cc, int grp, uint32_t keep, int lo, int hi, float sgn) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            // B: matrix m = keys 8 (m >> 1) .., first (m even) or second half of the group
+            const int key = 32 * cc + 16 * half + 8 * (qm >> 1) + qi;
+            const int ch = (qm & 1) ? P / 8 + grp : grp;
+            uint32_t b00, b01, b10, b11;
+            ldsm_x4(kb + (key >> 3) * L::GROUP + (ch >> 3) * 1024 + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
+                    b00, b01, b10, b11);
+            float acc[2][2][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const uint32_t a0 = afr[mt][0] & keep, a1 = afr[mt][1] & keep;
+              const uint32_t a2 = afr[mt][2] & keep, a3 = afr[mt][3] & keep;
+              mma_16816_bf16(acc[mt][0], a0, a1, a2, a3, b00, b01);
+              mma_16816_bf16(acc[mt][1], a0, a1, a2, a3, b10, b11);
+            }
+            __syncwarp();                      // the scratch's previous rows have been read
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) {
+                const int rr = 16 * mt + (lane >> 2), cl = 8 * nt + 2 * (lane & 3);
+                *reinterpret_cast<float2*>(scr + rr * 16 + cl) = make_float2(acc[mt][nt][0], acc[mt][nt][1]);
+                *reinterpret_cast<float2*>(scr + (rr + 8) * 16 + cl) = make_float2(acc[mt][nt][2], acc[mt][nt][3]);
+              }
+            __syncwarp();
+            const float4* mine = reinterpret_cast<const float4*>(scr + lane * 16);
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+              const float4 x = mine[c4];
+              const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = 16 * half + 4 * c4 + e;
+                if (c >= lo && c <= hi) v[c] = fmaf(sgn, xs[e], v[c]);
+              }
+            }
+          }
+        };
+        if constexpr (G8) {
+          // whole groups of 8 pairs share a threshold
+#pragma unroll 1
+          for (int gp = plo; gp < P; gp += 8) {
+            const bool sub = gp >= ps;
+            const int T = sT[gp];
+            // columns of this row that take the group's term
+            const int c_lo = sub || T >= d_row ? 0 : d_row - T;
+            const int c_hi = !sub ? min(d_row, 127) : d_row > T ? min(d_row - T - 1, 127) : -1;
+            if (!__any_sync(FULL, c_lo <= c_hi)) {
+              if (sub) break;                  // later groups are pruned at even fewer columns
+              continue;
+            }
+            load_a(gp >> 3);
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              const int lo = c_lo - 32 * cc, hi = c_hi - 32 * cc;
+              if (!__any_sync(FULL, lo <= 31 && hi >= 0 && lo <= hi)) continue;
+              float v[32];
+              tmem_ld32(tS + 32 * cc, v);
+              tmem_ld_wait();
+              apply(v, cc, gp >> 3, 0xFFFFFFFFu, lo, hi, sub ? -1.f : 1.f);
+              tmem_st32(tS + 32 * cc, v);
+            }
+          }
+        } else {
+          const int T_lo = ps > plo ? sT[ps - 1] : 0;
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            const int dc = d_row - 32 * cc;                  // distance at the chunk's first column
+            const int dmax = __shfl_sync(FULL, dc, 31);      // largest and smallest of the block
+            const int dmin = max(__shfl_sync(FULL, dc, 0) - 31, 0);
+            if (dmax < 0) continue;                          // wholly acausal
+            // pairs ps .. pb - 1 are pruned somewhere in the block, pa .. ps - 1 kept somewhere
+            int pb = ps, pa = ps;
+            if (need_sub)
+              while (pb < P && sT[pb] < dmax) ++pb;
+            if (need_add && T_lo >= dmin)
+              while (pa > plo && sT[pa - 1] >= dmin) --pa;
+            if (pa >= pb) continue;
+            float v[32];
+            tmem_ld32(tS + 32 * cc, v);
+            tmem_ld_wait();
+            int cur = -1;
+#pragma unroll 1
+            for (int pp = pa; pp < pb; ++pp) {
+              if ((pp >> 3) != cur) load_a(cur = pp >> 3);
+              const int T = sT[pp];
+              const bool sub = pp >= ps;
+              const int lo = sub || T >= dc ? 0 : dc - T;
+              const int hi = !sub ? min(dc, 31) : dc > T ? min(dc - T, 32) - 1 : -1;
+              if (!__any_sync(FULL, lo <= hi)) continue;
+              // a lane's A register halves hold pairs 8 grp + 2 (lane & 3) (+ 1)
+              const int jp = pp & 7;
+              const uint32_t keep = ((lane & 3) == (jp >> 1)) ? ((jp & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+              apply(v, cc, cur, keep, lo, hi, sub ? -1.f : 1.f);
+            }
+            tmem_st32(tS + 32 * cc, v);
+          }
+        }
+        tmem_st_wait();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(stage_empty);
+      }
+      float sc[128];
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, &sc[32 * cc]);
+      tmem_ld_wait();
+      // the loaded values are only defined after the wait: keep every use below it
+#pragma unroll
+      for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(sc[c]));
+      if (all_pruned) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) sc[c] = 0.f;   // every pair pruned: score 0
+      }
+      // causal mask (d < 0) and the sequence's end: columns c > cm
+      if (q_first(t) - (kp0 + 127) < 0 || kp0 + 128 > it.kv_len) {
+        const int cm = min(max(min(d_row, it.kv_len - 1 - kp0), -1), 128);
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > cm) sc[c] = -INFINITY;
+      }
+      // row max, then the exponentials against the (lazily moved) reference
+      const float sl = p.scale_log2;
+      float mt;
+      {
+        float a16[16], b6[6];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          a16[k] = max3(max3(sc[8 * k], sc[8 * k + 1], sc[8 * k + 2]), max3(sc[8 * k + 3], sc[8 * k + 4], sc[8 * k + 5]),
+                        fmaxf(sc[8 * k + 6], sc[8 * k + 7]));
+#pragma unroll
+        for (int k = 0; k < 5; ++k) b6[k] = max3(a16[3 * k], a16[3 * k + 1], a16[3 * k + 2]);
+        b6[5] = a16[15];
+        mt = fmaxf(max3(b6[0], b6[1], b6[2]), max3(b6[3], b6[4], b6[5])) * sl;
+      }
+      // the reference moves only when the max grew by more than 8 (x256);
+      // s_full implies that this tile's previous PV has completed
+      float f = 1.f;
+      if (cnt == 0) {
+        m_ref = mt;
+      } else if (mt > m_ref + 8.f) {
+        f = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - mt);
+        m_ref = mt;
+      }
+      if (cnt > 0 && __any_sync(FULL, f != 1.f)) {
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          float o[32];
+          tmem_ld32(tO + 32 * cc, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= f;
+          tmem_st32(tO + 32 * cc, o);
+        }
+      }
+      uint32_t pk2[64];                        // p, rounded to bf16 (the MMA's operand type); l sums them unrounded
+      {
+        const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        float acc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          float x0, x1;
+          fma2(x0, x1, sc[2 * i], sc[2 * i + 1], sl, sl, nm, nm);
+          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+          add2(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], acc[2 * (i & 3)], acc[2 * (i & 3) + 1], e0, e1);
+          pk2[i] = pack_bf16x2(e0, e1);
+        }
+        l_run = l_run * f + (((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
+      }
+      tmem_st32u(tS, &pk2[0]);                 // P overwrites the first 64 columns of S
+      tmem_st32u(tS + 32, &pk2[32]);
+      if (more) write_masked_q(ps_next);       // before P is released to the MMA warp
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(t));
+      ++cnt;
+    }
+
+    // ----------------------------------------------------------- epilogue
+    if (steps > 0) {                           // every MMA of both tiles has completed
+      (void)__all_sync(FULL, mbar_wait(o_final(t), 0));
+      tc_fence_after();
+    }
+    const bool split = it.parts > 1;
+    // dup: group 1 hands its half over through the ring, which every MMA has left
+    float* half = reinterpret_cast<float*>(smem);            // [D][128 rows]
+    float2* half_ml = reinterpret_cast<float2*>(smem + 128 * D * 4);   // (m, l)
+    if (dup) {
+      if (t == 1) {
+        half_ml[r] = make_float2(m_ref, l_run);
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          if (cnt == 0) break;
+          float o[32];
+          tmem_ld32(tO + 32 * cc, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) half[(32 * cc + e) * 128 + r] = o[e];
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    if (!(dup && t == 1)) {
+      float w0 = 1.f, w1 = 0.f;                // weights of this group's O and of the other's
+      if (dup) {
+        const float2 other = half_ml[r];
+        const float M = fmaxf(m_ref, other.x);
+        if (M != -INFINITY) {
+          w0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - M);
+          w1 = other.x == -INFINITY ? 0.f : ex2_approx(other.x - M);
+        }
+        l_run = l_run * w0 + other.y * w1;
+        m_ref = M;
+      }
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      w0 *= inv;
+      w1 *= inv;
+      const bool both = dup && steps > 1;      // group 1 had a key tile
+      const size_t prow = static_cast<size_t>(blockIdx.x) * 256 + t * 128 + r;
+      float* po = p.part_o + (static_cast<size_t>(blockIdx.x) * (D / 8) * 256 + t * 128 + r) * 8;
+      uint16_t* orow = p.out + qrow * D;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        float o[32];
+        if (cnt > 0) {
+          tmem_ld32(tO + 32 * cc, o);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          o[e] = cnt > 0 ? o[e] * w0 : 0.f;
+          if (both) o[e] = fmaf(half[(32 * cc + e) * 128 + r], w1, o[e]);
+        }
+        if (!row_ok) continue;
+        if (split) {
+#pragma unroll
+          for (int c8 = 0; c8 < 4; ++c8) {
+            float4* dst = reinterpret_cast<float4*>(po + static_cast<size_t>(4 * cc + c8) * 256 * 8);
+            dst[0] = make_float4(o[8 * c8], o[8 * c8 + 1], o[8 * c8 + 2], o[8 * c8 + 3]);
+            dst[1] = make_float4(o[8 * c8 + 4], o[8 * c8 + 5], o[8 * c8 + 6], o[8 * c8 + 7]);
+          }
+        } else {
+#pragma unroll
+          for (int c8 = 0; c8 < 4; ++c8)
+            *reinterpret_cast<uint4*>(orow + 32 * cc + 8 * c8) =
+                make_uint4(pack_bf16x2(o[8 * c8], o[8 * c8 + 1]), pack_bf16x2(o[8 * c8 + 2], o[8 * c8 + 3]),
+                           pack_bf16x2(o[8 * c8 + 4], o[8 * c8 + 5]), pack_bf16x2(o[8 * c8 + 6], o[8 * c8 + 7]));
+        }
+      }
+      const float l2 = l_run > 0.f ? m_ref + __log2f(l_run) : -INFINITY;
+      if (row_ok && split) p.part_l[prow] = l2;
+      else if (row_ok && p.lse) p.lse[qrow] = l2 * 0.69314718055994530942f;
+    }
+  }
+
   __syncwarp();
-  const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-  float m = -INFINITY, l = 0.f, o[E] = {};
-  for (int j0 = 0; j0 <= pos; j0 += 32) {
-    const int j = j0 + lane;
-    size_t at = 0;                          // element offset of this lane's key
-    float s = -INFINITY;
-    if (j <= pos) {
-      const int pg = checked_page(table[j / p.page_size], p.num_pages);
-      at = ((static_cast<size_t>(pg) * p.page_size + j % p.page_size) * p.Hkv + kvh) * D;
-      s = 0.f;
-      for (int pp = 0; pp < P; ++pp)
-        if (pos - j <= p.T[pp])
-          s = fmaf(sq[warp][pp], bf16lo_to_f32(p.k[at + pp]),
-                   fmaf(sq[warp][pp + P], bf16lo_to_f32(p.k[at + pp + P]), s));
-      s *= p.scale_log2;
-    }
-    float bm = s;
-    for (int off = 16; off > 0; off >>= 1) bm = fmaxf(bm, __shfl_xor_sync(FULL, bm, off));
-    const float mn = fmaxf(m, bm);
-    const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
-    const float w = mn == -INFINITY ? 0.f : ex2_approx(s - mn);
-    m = mn;
-    l = l * f + w;
-    for (int e = 0; e < E; ++e) o[e] *= f;
-    for (int i = 0; i < 32 && j0 + i <= pos; ++i) {
-      const float wi = __shfl_sync(FULL, w, i);
-      const size_t ai = __shfl_sync(FULL, static_cast<unsigned long long>(at), i);
-      for (int e = 0; e < E; ++e) o[e] = fmaf(wi, bf16lo_to_f32(p.v[ai + lane + 32 * e]), o[e]);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == W_MMA) tmem_dealloc(tmem, 512);
+}
+
+// Merge of the parts of one row block: with w_s = 2^(l_s - max l), out = sum_s
+// w_s o_s / sum_s w_s.  Block (c, y): rows of CTA c, when it is its row
+// block's first part, dims 32 y .. 32 y + 31; a thread per row.
+template <int D, int MAXB>
+__global__ void __launch_bounds__(256)
+prefill_paged_merge_kernel(const __grid_constant__ PrefillPagedParams<MAXB> p) {
+  const int c = blockIdx.x;
+  const PagedItem it = paged_item(p, c);
+  if (it.part != 0) return;
+  const int t = threadIdx.x >> 7, r = threadIdx.x & 127;
+  const int tok = r / p.G;
+  if ((it.dup && t == 1) || r >= p.tile_tokens * p.G || tok >= it.ntok[t]) return;
+  const int tiles = (it.q_len + p.tile_tokens - 1) / p.tile_tokens;
+  const int step = ((tiles + 1) >> 1) * p.Hkv;             // CTAs from one part to the next
+  const float* pl = p.part_l + static_cast<size_t>(c) * 256 + threadIdx.x;
+  const float* po = p.part_o + ((static_cast<size_t>(c) * (D / 8) + 4 * blockIdx.y) * 256 + threadIdx.x) * 8;
+  float M = -INFINITY;
+  for (int s = 0; s < it.parts; ++s) M = fmaxf(M, pl[static_cast<size_t>(s) * step * 256]);
+  float W = 0.f, acc[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+  for (int s = 0; s < it.parts; ++s) {
+    const float ls = pl[static_cast<size_t>(s) * step * 256];
+    if (ls == -INFINITY) continue;                         // no key: its O was not written
+    const float w = ex2_approx(ls - M);
+    W += w;
+#pragma unroll
+    for (int e8 = 0; e8 < 4; ++e8) {
+      const float4* src = reinterpret_cast<const float4*>(po + (static_cast<size_t>(s) * step * (D / 8) + e8) * 256 * 8);
+      const float4 x = src[0], y = src[1];
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[8 * e8 + e] = fmaf(w, v[e], acc[8 * e8 + e]);
     }
   }
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(FULL, l, off);
-  for (int e = 0; e < E; ++e) {
-    const float val = l > 0.f ? o[e] / l : 0.f;
-    p.out[row * D + lane + 32 * e] = static_cast<uint16_t>(pack_bf16x2(val, 0.f) & 0xFFFFu);
+  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const size_t row = (static_cast<size_t>(it.row0) + it.tok[t] + tok) * p.Hq + static_cast<size_t>(it.kvh) * p.G + r % p.G;
+  uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + 32 * blockIdx.y);
+#pragma unroll
+  for (int e8 = 0; e8 < 4; ++e8) {
+    const float* a = acc + 8 * e8;
+    dst[e8] = make_uint4(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv),
+                         pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
   }
-  if (p.lse && lane == 0)
-    p.lse[row] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
+  if (p.lse && blockIdx.y == 0) p.lse[row] = W > 0.f ? (M + __log2f(W)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace wpattn
