@@ -147,8 +147,7 @@ float wave_time(const int* count, const float* cost, int n, int slots) {
   return lv[m - 1].t + rest;
 }
 
-// Costs are in steps of a two-tile row block (a key tile for both: 1.7 us at D =
-// 128).  A one-tile block's step costs kDupStep of one, a CTA's start and end
+// Costs are in steps of a two-tile row block (a tile of 128 keys for both).  A one-tile block's step costs kDupStep of one, a CTA's start and end
 // kCtaSteps, the merge pass kMergeSteps.  The length of a part is the one
 // whose grid these say is done first, out of those that make about 1 .. 12
 // waves of the whole work, and no split at all.

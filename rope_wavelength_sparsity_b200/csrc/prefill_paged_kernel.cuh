@@ -23,12 +23,14 @@
 //   warps 0-3, 4-7  softmax of tile 0 / 1: row r is TMEM lane r.  They bring Q
 //              in, correct the pairs kept at some but not all distances of a
 //              tile, mask, run the online softmax, write P (bf16) over S.
-//   warp 8     TMA producer: lane u copies unit u of a key tile (R keys of one
-//              page, R = the largest power of two that divides the page, up
-//              to 128), K and V by one copy each.
-//   warp 9     MMA issuer (one lane); owns the TMEM allocation.
-//   warp 10    zeroes the V rows behind the sequence's last key, which may
-//              hold anything (0 * NaN would reach every row's output).
+//   warps 8, 11  TMA producers of K and V: lane u copies unit u of a key tile
+//              (R keys of one page, R = the largest power of two that divides
+//              the page, up to 128).  One warp issues a copy every 40-54 ns,
+//              whatever its size; 16-key pages need 16 a step, so K and V have
+//              a warp each.
+//   warps 9, 10  MMA issuers of tile 0 / 1 (one alone was the bound: its issue
+//              and waits took 3900 cycles a step); warp 9 owns the TMEM.
+//   The V producer also zeroes the V rows behind the sequence's last key.
 //
 // Shared-memory layouts.  K and V tiles are groups of 8 keys, each D / 64
 // panels of 8 rows x 128 bytes, 128-byte swizzled: the layout one 4-D copy
@@ -39,8 +41,14 @@
 // half, and a unit of 16 pairs is two steps.  Q is no-swizzle K-major:
 // 16-byte columns of 128 rows, 2 KB apart.
 //
-// TMEM columns: S_t / P_t at [128 t, 128 t + 128), O_t at 256 + t D.
+// TMEM columns: each tile has two score buffers of 64 keys, 64 columns wide, at
+// 128 t (P, bf16, over the first half of each), so that the scores of a key
+// tile are computed while the softmax works on the one before it: with one
+// buffer a step was the sum of its softmax and of its products (4400 cycles
+// for 128 keys; exponentials alone take 2048, products 2100).  O_t at 256 + t D.
 #pragma once
+
+#include <type_traits>
 
 #include "device_util.cuh"
 #include "prefill_kernel.cuh"
@@ -124,25 +132,72 @@ __device__ __forceinline__ int checked_page(int pg, int num_pages) {
 
 template <int D>
 struct PagedSmem {
-  static constexpr int NSK = D == 64 ? 4 : 2;        // K ring; one more when `dup` leaves tile 1's Q free
-  static constexpr int NSV = NSK;
-  static constexpr int TILE = 128 * D * 2;           // a tile of K, V or Q
+  static constexpr int KT = 128;                     // keys of a key tile
+  // K and V ring depths: even, so that with `dup` a stage's steps all belong to
+  // one row tile.  A row tile's warps follow their own steps only, and a parity
+  // wait cannot tell a phase from the one after next.
+  static constexpr int NSK = D == 64 ? 4 : 2, NSV = NSK;
+  static constexpr int TILE = KT * D * 2;            // a tile of K or V
   static constexpr int GROUP = 8 * D * 2;            // 8 keys
   static constexpr int COL = 128 * 16;               // 16-byte column of Q
   static constexpr int OFF_V = 0;
-  static constexpr int OFF_K = OFF_V + NSV * TILE;
+  static constexpr int OFF_K = NSV * TILE;
   static constexpr int OFF_Q1 = OFF_K + NSK * TILE;
-  static constexpr int OFF_Q0 = OFF_Q1 + TILE;
-  static constexpr int OFF_QM = OFF_Q0 + TILE;       // per tile: Q's first unit with its left-out pairs zeroed
+  static constexpr int OFF_Q0 = OFF_Q1 + 128 * D * 2;
+  static constexpr int OFF_QM = OFF_Q0 + 128 * D * 2;    // per tile: Q's first unit with its left-out pairs zeroed
   static constexpr int OFF_SCR = OFF_QM + 2 * 4 * COL;   // per warp [32 rows][16 keys] fp32
   static constexpr int OFF_T = OFF_SCR + 8 * 2048;
-  static constexpr int OFF_BAR = OFF_T + 64 * 4;
-  // k_full, k_empty [NSK + 1], v_full, v_empty [NSV], s_full, p_full, o_final, q_ready [2], v_fix
-  static constexpr int NBAR = 2 * (NSK + 1) + 2 * NSV + 9;
+  static constexpr int OFF_PS = OFF_T + 64 * 4;      // plan of each tile's next step
+  static constexpr int OFF_LEFT = OFF_PS + 4 * 4;    // warps of each softmax group that left a corrected K tile
+  static constexpr int OFF_BUSY = OFF_LEFT + 4 * 4;  // softmax warps at their exponentials
+  static constexpr int OFF_BAR = OFF_BUSY + 8 * 4;
+  // k_full, k_empty [NSK], v_full, v_empty [NSV], s_full, p_half, p_full, o_final, q_ready [2], v_fix
+  static constexpr int NBAR = 2 * NSK + 2 * NSV + 11;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_TMEM + 16;
 };
+static_assert(PagedSmem<64>::NSK % 2 == 0 && PagedSmem<128>::NSK % 2 == 0, "even rings");
 static_assert(PagedSmem<128>::ALLOC <= 232448 && PagedSmem<64>::ALLOC <= 232448, "shared memory of one CTA");
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one)::"memory");
+  return one;
+}
+
+// The products and commits of a whole, converged warp, issued by the lane whose
+// `leader` is 1.  Every operand is the same in all lanes, so that the
+// compiler can keep them in uniform registers, where the instructions take
+// them from; in a one-lane branch each product cost 75 cycles to issue.  A
+// descriptor's upper word is a constant, its lower one an address in
+// 16-byte units plus a constant.
+__device__ __forceinline__ void warp_mma_ss(uint32_t leader, uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo,
+                                            uint32_t bhi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 p, %7, 0;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %6, p;\n\t}" ::"r"(leader),
+      "r"(d), "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 q, %0, 0;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %5, p;\n\t}" ::"r"(leader),
+      "r"(d), "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader),
+      "r"(bar)
+      : "memory");
+}
 
 template <int D, bool G8, int MAXB>
 __global__ void __launch_bounds__(384, 1)
@@ -150,25 +205,28 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                      const __grid_constant__ PrefillPagedParams<MAXB> p) {
   using L = PagedSmem<D>;
   constexpr int P = D / 2;
-  constexpr int NSV = L::NSV, TILE = L::TILE, COL = L::COL;
-  constexpr int W_PROD = 8, W_MMA = 9, W_FIX = 10;
+  constexpr int KT = L::KT, NSK = L::NSK, NSV = L::NSV, TILE = L::TILE, COL = L::COL;
+  constexpr int W_PROD_K = 8, W_MMA = 9, W_PROD_V = 11;   // W_MMA + t issues tile t's products
   constexpr uint32_t TMEM_O = 256;
+  constexpr int kCorr = 1 << 8;         // of a step's plan (split pair + this): scores need corrections
   constexpr uint32_t FULL = 0xffffffffu;
 
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar = sbase + L::OFF_BAR;
   auto k_full = [&](int s) { return bar + 8 * s; };
-  auto k_empty = [&](int s) { return bar + 8 * (L::NSK + 1 + s); };
-  auto v_full = [&](int s) { return bar + 8 * (2 * L::NSK + 2 + s); };
-  auto v_empty = [&](int s) { return bar + 8 * (2 * L::NSK + 2 + NSV + s); };
-  constexpr int B0 = 2 * L::NSK + 2 + 2 * NSV;
+  auto k_empty = [&](int s) { return bar + 8 * (NSK + s); };
+  auto v_full = [&](int s) { return bar + 8 * (2 * NSK + s); };
+  auto v_empty = [&](int s) { return bar + 8 * (2 * NSK + NSV + s); };
+  constexpr int B0 = 2 * NSK + 2 * NSV;
   auto s_full = [&](int t) { return bar + 8 * (B0 + t); };
-  auto p_full = [&](int t) { return bar + 8 * (B0 + 2 + t); };
-  auto o_final = [&](int t) { return bar + 8 * (B0 + 4 + t); };
-  auto q_ready = [&](int t) { return bar + 8 * (B0 + 6 + t); };
-  const uint32_t v_fix = bar + 8 * (B0 + 8);
+  auto p_half = [&](int t) { return bar + 8 * (B0 + 2 + t); };
+  auto p_full = [&](int t) { return bar + 8 * (B0 + 4 + t); };
+  auto o_final = [&](int t) { return bar + 8 * (B0 + 6 + t); };
+  auto q_ready = [&](int t) { return bar + 8 * (B0 + 8 + t); };
+  const uint32_t v_fix = bar + 8 * (B0 + 10);
   int* sT = reinterpret_cast<int*>(smem + L::OFF_T);
+  volatile int* sPS = reinterpret_cast<volatile int*>(smem + L::OFF_PS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM);
 
   // the swizzled tiles need a 1024-byte aligned shared window
@@ -179,52 +237,37 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedItem it = paged_item(p, blockIdx.x);
   const bool dup = it.dup;
-  const int nkt = (it.kv_len + 127) >> 7;
+  const int nkt = (it.kv_len + KT - 1) / KT;
   const int per = (nkt + it.parts - 1) / it.parts;
   const int kt_lo = it.part * per, kt_hi = min(kt_lo + per, nkt) - 1;
   const int pos0 = it.kv_len - it.q_len;              // the chunk's first position
-  auto q_first = [&](int t) { return pos0 + it.tok[t]; };
+  auto q_first = [&](int t) { return pos0 + (t == 0 ? it.tok[0] : it.tok[1]); };
   // key tiles of row tile t: kt_lo .. kt_last[t], walked downwards; none: kt_lo - 1
   int kt_last[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int i_max = q_first(t) + it.ntok[t] - 1;
-    kt_last[t] = i_max < 0 ? kt_lo - 1 : max(min(i_max >> 7, kt_hi), kt_lo - 1);
+    kt_last[t] = i_max < 0 ? kt_lo - 1 : max(min(i_max / KT, kt_hi), kt_lo - 1);
   }
   const int top = max(kt_last[0], kt_last[1]);
   const int steps = top - kt_lo + 1;                  // step j is key tile top - j
   auto attends = [&](int t, int j) { return dup ? (j & 1) == t : top - j <= kt_last[t]; };
-  const int nsk = L::NSK + (dup ? 1 : 0);
-  const bool tail = steps > 0 && top == nkt - 1 && (it.kv_len & 127) != 0;
-
-  // First pair kept somewhere in a tile (only moves forward along the walk).
-  auto advance_plo = [&](int t, int kt, int& plo) {
-    const int dlo = q_first(t) - (128 * kt + 127);
-    while (plo < P && sT[plo] < dlo) ++plo;
-  };
-  // Split pair: pairs plo .. ps - 1 are left out of the contraction and added
-  // back where they are kept; pairs ps .. P - 1 are contracted and subtracted
-  // where they are pruned.  At the pair first kept 32 past the tile's centre
-  // distance both sets are small (thresholds grow geometrically).
-  auto split_pair = [&](int t, int kt, int plo, int& psr) -> int {
-    if (plo >= P) return plo;
-    const int dc = max(q_first(t) - 128 * kt + (p.tile_tokens >> 1) - 64, 0);
-    while (psr < P && sT[psr] < dc + 32) ++psr;
-    return min(max(psr, plo), P - (G8 ? 8 : 1));
-  };
+  const bool tail = steps > 0 && top == nkt - 1 && it.kv_len % KT != 0;
 
   if (threadIdx.x < 64) sT[threadIdx.x] = p.T[threadIdx.x];
+  if (threadIdx.x < 12) reinterpret_cast<int*>(smem + L::OFF_LEFT)[threadIdx.x] = 0;   // OFF_BUSY too
   if (threadIdx.x == 0) {
-    for (int s = 0; s <= L::NSK; ++s) {
+    for (int s = 0; s < NSK; ++s) {
       mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), dup ? 5 : 9);   // MMA commit + the softmax warps that attend the stage
+      mbar_init(k_empty(s), dup ? 1 : 2);   // a release by each row tile that takes the stage
     }
     for (int s = 0; s < NSV; ++s) {
       mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
+      mbar_init(v_empty(s), dup ? 1 : 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 1);
+      mbar_init(p_half(t), 4);
       mbar_init(p_full(t), 4);
       mbar_init(o_final(t), 1);
       mbar_init(q_ready(t), 4);
@@ -239,149 +282,33 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0;          // an allocation of all 512 columns starts at the first
 
-  if (warp >= W_PROD) {
+  if (warp >= 8) {
     regs_decrease<56>();
-    if (warp == W_PROD) {
-      // ---------------------------------------------------------- producer
-      const int R = p.unit, units = 128 / R;
+    if (warp == W_PROD_K || warp == W_PROD_V) {
+      // --------------------------------------------------------- producers
+      const bool is_k = warp == W_PROD_K;
+      const CUtensorMap* map = is_k ? &tmK : &tmV;
+      const uint32_t ring = sbase + (is_k ? L::OFF_K : L::OFF_V);
+      const uint32_t full = is_k ? k_full(0) : v_full(0), empty = is_k ? k_empty(0) : v_empty(0);
+      constexpr int stages = NSK;
+      const int R = p.unit, units = KT / R;
       const int32_t* table = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
       // this lane's unit of key tile kt: its 8-key group in the pool, -1: no key
       auto fetch = [&](int kt) -> int {
-        const int key = 128 * kt + lane * R;
+        const int key = KT * kt + lane * R;
         if (kt < kt_lo || lane >= units || key >= it.kv_len) return -1;
         const int pg = checked_page(__ldg(table + key / p.page_size), p.num_pages);
         return (pg * p.page_size + key % p.page_size) >> 3;
       };
-      if (lane == 0) {
-        prefetch_tensormap(&tmK);
-        prefetch_tensormap(&tmV);
-      }
-      int next = fetch(top), nk = 0, nv = 0;   // nk, nv: tiles whose copies were issued
-      bool ok = true;
-      int sk = 0, pk = 0;
-      for (int j = 0; j < steps; ++j) {
-        const int at = next, kt = top - j, sv = j % NSV;
-        const uint32_t bytes = __popc(__ballot_sync(FULL, at >= 0)) * R * D * 2;
-        if (j >= nsk && !__all_sync(FULL, mbar_wait(k_empty(sk), pk ^ 1))) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(k_full(sk), bytes);
-        __syncwarp();
-        if (at >= 0)
-          tma_load_4d(sbase + L::OFF_K + sk * TILE + lane * R * D * 2, &tmK, k_full(sk), 0, 0, it.kvh * (D / 64), at);
-        nk = j + 1;
-        if (++sk == nsk) { sk = 0; pk ^= 1; }
-        next = fetch(kt - 1);
-        if (j >= NSV && !__all_sync(FULL, mbar_wait(v_empty(sv), ((j / NSV) & 1) ^ 1))) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(v_full(sv), bytes);
-        __syncwarp();
-        if (at >= 0)
-          tma_load_4d(sbase + L::OFF_V + sv * TILE + lane * R * D * 2, &tmV, v_full(sv), 0, 0, it.kvh * (D / 64), at);
-        nv = j + 1;
-      }
-      if (!ok) {
-        // A wait ran out: wait (bounded) for the copies that may still be landing
-        for (int j = max(0, nk - nsk); j < nk; ++j) (void)mbar_wait(k_full(j % nsk), (j / nsk) & 1);
-        for (int j = max(0, nv - NSV); j < nv; ++j) (void)mbar_wait(v_full(j % NSV), (j / NSV) & 1);
-      }
-    } else if (warp == W_MMA) {
-      // -------------------------------------------------------- MMA issuer
-      if (lane == 0 && steps > 0) {
-        constexpr uint32_t idesc_qk = make_idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t idesc_pv = make_idesc_bf16(128, D, 0, 1);
-        const uint64_t qdesc = make_sdesc(sbase + L::OFF_Q0, COL, 128, 0);
-        const uint64_t q1desc = make_sdesc(sbase + L::OFF_Q1, COL, 128, 0);
-        const uint64_t qmdesc = make_sdesc(sbase + L::OFF_QM, COL, 128, 0);
-        const uint64_t kdesc = make_sdesc(sbase + L::OFF_K, 16, L::GROUP, 2);
-        const uint64_t vdesc = make_sdesc(sbase + L::OFF_V, 1024, L::GROUP, 2);
-        const int ahead = dup ? 2 : 1;         // a tile's next QK follows its PV
-        int cnt[2] = {0, 0}, plo[2] = {0, 0}, psr[2] = {0, 0};
-        bool q_seen[2] = {false, false};
-        bool ok = true;
-        int sk = 0, pk = 0;                    // ring position of the next QK's key tile
-        auto plan_qk = [&](int t, int j) -> int {
-          advance_plo(t, top - j, plo[t]);
-          return split_pair(t, top - j, plo[t], psr[t]);
-        };
-        auto issue_qk = [&](int t, int ps) -> bool {
-          if (!q_seen[t]) {
-            if (!mbar_wait(q_ready(t), 0)) return false;
-            q_seen[t] = true;
-            tc_fence_after();
-          }
-          const uint64_t kb = kdesc + static_cast<uint64_t>((sk * TILE) >> 4);
-          const uint64_t qb = (dup || t == 0) ? qdesc : q1desc;
-          const int u0 = ps >> 4;
-          for (int u = u0; u < P / 16; ++u) {
-            const bool masked = u == u0 && (ps & 15);
-            const uint64_t a = masked ? qmdesc + static_cast<uint64_t>((t * 4 * COL) >> 4)
-                                      : qb + static_cast<uint64_t>((2 * u * COL) >> 4);
-            const uint64_t a2 = a + static_cast<uint64_t>(((masked ? 2 : D / 16) * COL) >> 4);
-            // the unit's second halves: the next 64-dim panel (D = 128), or 64 bytes on (D = 64)
-            const uint64_t b = kb + static_cast<uint64_t>((u * 32) >> 4);
-            const uint64_t b2 = b + static_cast<uint64_t>((D == 128 ? 1024 : 64) >> 4);
-            umma_ss(tmem + t * 128, a, b, idesc_qk, u > u0 ? 1u : 0u);
-            umma_ss(tmem + t * 128, a2, b2, idesc_qk, 1u);
-          }
-          umma_commit(s_full(t));
-          return true;
-        };
-        for (int j = 0; ok && j < min(ahead, steps); ++j) {
-          ok = mbar_wait(k_full(sk), pk);
-          tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (ok && attends(t, j)) ok = issue_qk(t, plan_qk(t, j));
-          if (!ok) break;
-          umma_commit(k_empty(sk));
-          if (++sk == nsk) { sk = 0; pk ^= 1; }
-        }
-        for (int j = 0; ok && j < steps; ++j) {
-          const int jn = j + ahead, sv = j % NSV;
-          const bool next = jn < steps;
-          if (!mbar_wait(v_full(sv), (j / NSV) & 1)) { ok = false; break; }
-          if (tail && j == 0 && !mbar_wait(v_fix, 0)) { ok = false; break; }
-          const uint64_t vb = vdesc + static_cast<uint64_t>((sv * TILE) >> 4);
-          bool k_seen = false;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const bool do_qk = ok && next && attends(t, jn);
-            const int ps = do_qk ? plan_qk(t, jn) : 0;
-            if (ok && attends(t, j)) {
-              if (!mbar_wait_handoff(p_full(t), cnt[t] & 1)) ok = false;
-              if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                  umma_ts(tmem + TMEM_O + t * D, tmem + t * 128 + ks * 8,
-                              vb + static_cast<uint64_t>((ks * 2 * L::GROUP) >> 4), idesc_pv,
-                              (cnt[t] > 0 || ks > 0) ? 1u : 0u);
-                ++cnt[t];
-              }
-            }
-            if (ok && do_qk) {
-              if (!k_seen) {
-                ok = mbar_wait_handoff(k_full(sk), pk);
-                k_seen = true;
-              }
-              ok = ok && issue_qk(t, ps);
-            }
-          }
-          if (!ok) break;
-          umma_commit(v_empty(sv));
-          if (next) {
-            umma_commit(k_empty(sk));
-            if (++sk == nsk) { sk = 0; pk ^= 1; }
-          }
-        }
-        // every MMA issued so far has completed once these arrive
-        for (int t = 0; t < 2; ++t) umma_commit(o_final(t));
-        if (!ok) mbar_wait(o_final(0), 0);
-      }
-    } else if (warp == W_FIX && tail) {
-      if (__all_sync(FULL, mbar_wait(v_full(0), 0))) {
+      if (lane == 0) prefetch_tensormap(map);
+      // V rows behind the sequence's last key may hold anything, and 0 * NaN would
+      // reach every row's output: they are zeroed once the first tile is there
+      auto zero_tail = [&]() {
+        if (!__all_sync(FULL, mbar_wait(v_full(0), 0))) return;
         constexpr int ROW_CHUNKS = D / 8;
-        for (int i = (it.kv_len & 127) * ROW_CHUNKS + lane; i < 128 * ROW_CHUNKS; i += 32) {
+        for (int i = it.kv_len % KT * ROW_CHUNKS + lane; i < KT * ROW_CHUNKS; i += 32) {
           const int row = i / ROW_CHUNKS, c = i % ROW_CHUNKS;
           *reinterpret_cast<uint4*>(smem + L::OFF_V + (row >> 3) * L::GROUP + (c >> 3) * 1024 + (row & 7) * 128 +
                                     (c & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -389,7 +316,123 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_fix);
+      };
+      int next = fetch(top), issued = 0;       // issued: tiles whose copies were issued
+      int s = 0, ph = 0;
+      for (int j = 0; j < steps; ++j) {
+        if (tail && !is_k && j == stages) zero_tail();
+        const int at = next;
+        next = fetch(top - j - 1);
+        const uint32_t bytes = __popc(__ballot_sync(FULL, at >= 0)) * R * D * 2;
+        if (j >= stages && !__all_sync(FULL, mbar_wait(empty + 8 * s, ph ^ 1))) break;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+        __syncwarp();
+        if (at >= 0)
+          tma_load_4d(ring + s * TILE + lane * R * D * 2, map, full + 8 * s, 0, 0, it.kvh * (D / 64), at);
+        issued = j + 1;
+        if (++s == stages) { s = 0; ph ^= 1; }
       }
+      if (tail && !is_k && steps <= stages) zero_tail();
+      if (issued < steps)   // a wait ran out: wait (bounded) for the copies that may still be landing
+        for (int j = max(0, issued - stages); j < issued; ++j) (void)mbar_wait(full + 8 * (j % stages), (j / stages) & 1);
+    } else {
+      // ------------------------------------------------------- MMA issuers
+      const int t = warp - W_MMA;
+      constexpr uint32_t idesc_qk = make_idesc_bf16(128, KT, 0, 0);
+      constexpr uint32_t idesc_pv = make_idesc_bf16(128, D, 0, 1);
+      // descriptors: upper words (stride between 8-row groups, layout), lower words without the address
+      constexpr uint32_t HI = 1u << 14;        // descriptor version
+      constexpr uint32_t q_hi = HI | (128 >> 4), kv_hi = HI | (L::GROUP >> 4) | (2u << 29);
+      constexpr uint32_t q_lo = (COL >> 4) << 16, k_lo = 1u << 16, v_lo = (1024u >> 4) << 16;
+      const uint32_t leader = elect_one();
+      const int stride = dup ? 2 : 1;
+      const int j0 = dup ? t : top - (t == 0 ? kt_last[0] : kt_last[1]);
+      const int mine = j0 < steps ? (steps - 1 - j0) / stride + 1 : 0;   // this tile's steps
+      const uint32_t qa = q_lo | ((sbase + ((dup || t == 0) ? L::OFF_Q0 : L::OFF_Q1)) >> 4);
+      const uint32_t qma = q_lo | ((sbase + L::OFF_QM + t * 4 * COL) >> 4);
+      bool ok = true;
+      int sk = 0, pk = 0, sv = 0, pv = 0;      // ring positions of the next QK's and the next PV's tile
+      auto step_k = [&]() {
+        if (++sk == NSK) { sk = 0; pk ^= 1; }
+      };
+      auto step_v = [&]() {
+        if (++sv == NSV) { sv = 0; pv ^= 1; }
+      };
+      // steps that only the other tile takes: released once they are there
+      for (int j = 0; ok && j < min(j0, steps); ++j) {
+        if (!dup) {
+          ok = __all_sync(FULL, mbar_wait(k_full(sk), pk) && mbar_wait(v_full(sv), pv));
+          if (ok && leader) {
+            mbar_arrive(k_empty(sk));
+            mbar_arrive(v_empty(sv));
+          }
+        }
+        step_k();
+        step_v();
+      }
+      int plan = 0;                            // of the next QK's step
+      // ready for the next QK: its K is there, and the plan that the softmax group
+      // left beside its latest hand-over
+      auto prepare_qk = [&]() {
+        ok = ok && __all_sync(FULL, mbar_wait_handoff(k_full(sk), pk));
+        plan = __shfl_sync(FULL, sPS[t], 0);
+      };
+      // S of this tile's next step, over the pairs from the split pair on
+      auto issue_qk = [&]() {
+        const int ps = plan & 0xFF, u0 = ps >> 4;
+        const bool masked = (ps & 15) != 0;
+        const uint32_t ka = k_lo | ((sbase + L::OFF_K + sk * TILE) >> 4);
+#pragma unroll
+        for (int u = 0; u < P / 16; ++u) {
+          // the unit's second halves: the next 64-dim panel (D = 128), or 64 bytes on (D = 64)
+          constexpr int HALF = (D == 128 ? 1024 : 64) >> 4;
+          if (u == u0) {
+            const uint32_t a = masked ? qma : qa + ((2 * u * COL) >> 4);
+            const uint32_t a2 = masked ? qma + ((2 * COL) >> 4) : qa + (((2 * u + D / 16) * COL) >> 4);
+            warp_mma_ss(leader, t * KT, a, q_hi, ka + 2 * u, kv_hi, idesc_qk, 0);
+            warp_mma_ss(leader, t * KT, a2, q_hi, ka + 2 * u + HALF, kv_hi, idesc_qk, 1);
+          } else if (u > u0) {
+            warp_mma_ss(leader, t * KT, qa + ((2 * u * COL) >> 4), q_hi, ka + 2 * u, kv_hi, idesc_qk, 1);
+            warp_mma_ss(leader, t * KT, qa + (((2 * u + D / 16) * COL) >> 4), q_hi, ka + 2 * u + HALF, kv_hi, idesc_qk, 1);
+          }
+        }
+        warp_commit(leader, s_full(t));
+        if (plan < kCorr) warp_commit(leader, k_empty(sk));   // else the softmax group still reads K
+        step_k();
+        if (dup) step_k();
+      };
+      if (mine > 0) {
+        ok = ok && __all_sync(FULL, mbar_wait(q_ready(t), 0));
+        tc_fence_after();
+        prepare_qk();
+        if (ok) issue_qk();
+      }
+      for (int n = 0; ok && n < mine; ++n) {
+        ok = __all_sync(FULL, mbar_wait_handoff(v_full(sv), pv));
+        if (tail && n == 0 && j0 == 0) ok = ok && __all_sync(FULL, mbar_wait(v_fix, 0));
+        const uint32_t va = v_lo | ((sbase + L::OFF_V + sv * TILE) >> 4);
+        // P comes in two halves: the first one's product runs under the second's exponentials
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && __all_sync(FULL, mbar_wait_handoff(half ? p_full(t) : p_half(t), n & 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = half * KT / 32; ks < (half + 1) * KT / 32; ++ks)
+            warp_mma_ts(leader, TMEM_O + t * D, t * KT + ks * 8, va + ((ks * 2 * L::GROUP) >> 4), kv_hi, idesc_pv,
+                        (n > 0 || ks > 0) ? 1u : 0u);
+          if (half == 0 && n + 1 < mine) prepare_qk();
+        }
+        if (!ok) break;
+        if (n + 1 < mine) issue_qk();          // first: the softmax group waits for it
+        warp_commit(leader, v_empty(sv));
+        step_v();
+        if (dup) step_v();
+      }
+      // every product of this tile has completed once this arrives
+      warp_commit(leader, o_final(t));
+      if (!ok) (void)mbar_wait(o_final(t), 0);
+      __syncwarp();
     }
   } else {
     regs_increase<224>();
@@ -398,16 +441,17 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     const int wq = warp & 3;
     const int r = wq * 32 + lane;              // row of the tile = TMEM lane
     const int tok = r / p.G;
-    const bool row_ok = r < p.tile_tokens * p.G && tok < it.ntok[t];
-    const int i_pos = q_first(t) + min(tok, it.ntok[t] - 1);   // rows without a token walk with the last
-    const size_t qrow = (static_cast<size_t>(it.row0) + it.tok[t] + (row_ok ? tok : 0)) * p.Hq +
+    const int tok0 = t == 0 ? it.tok[0] : it.tok[1], ntok = t == 0 ? it.ntok[0] : it.ntok[1];
+    const bool row_ok = r < p.tile_tokens * p.G && tok < ntok;
+    const int i_pos = q_first(t) + min(tok, ntok - 1);   // rows without a token walk with the last
+    const size_t qrow = (static_cast<size_t>(it.row0) + tok0 + (row_ok ? tok : 0)) * p.Hq +
                         static_cast<size_t>(it.kvh) * p.G + (row_ok ? r % p.G : 0);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t tS = lane_base + t * 128;
     const uint32_t tO = lane_base + TMEM_O + t * D;
     uint8_t* smem_q = smem + ((dup || t == 0) ? L::OFF_Q0 : L::OFF_Q1);
     uint8_t* smem_qm = smem + L::OFF_QM + t * 4 * COL;
-    const int my_last = kt_last[t];
+    const int my_last = t == 0 ? kt_last[0] : kt_last[1];
+    volatile int* busy = reinterpret_cast<volatile int*>(smem + L::OFF_BUSY);
     float m_ref = -INFINITY;   // exponent reference of O and l (log2 units)
     float l_run = 0.f;
     int cnt = 0;
@@ -422,6 +466,42 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");   // dup: group 1 reads group 0's rows
 
+    // The first pair kept somewhere in step j (plo) and the split pair (ps) of a pair
+    // of steps only move forward along the walk; each carries its threshold.
+    struct Cursor { int pair, T; };
+    auto advance = [&](Cursor& c, int d) {     // to the first pair whose threshold is at least d
+      while (c.pair < P && c.T < d) {
+        ++c.pair;
+        c.T = c.pair < P ? sT[c.pair] : 0x7FFFFFFF;
+      }
+    };
+    const int q0 = pos0 + tok0;                // positions of the tile's first and last row
+    const int q1 = q0 + ntok - 1;
+    auto nearest = [&](int j) { return q0 - (KT * (top - j) + KT - 1); };   // smallest distance of step j
+    // Split pair of a step: pairs plo .. ps - 1 are
+    // left out of the contraction and added back where they are kept; pairs ps
+    // .. P - 1 are contracted and subtracted where they are pruned.  At the
+    // pair first kept 32 past the tile's centre distance both sets are small
+    // (thresholds grow geometrically).  Any ps >= plo gives the same scores.
+    const int stride = dup ? 2 : 1;            // this tile's steps: every stride-th from j0 on
+    const int j0 = dup ? t : top - my_last;
+    Cursor low{0, sT[0]}, far = low;
+    int ps_now = P, T_ps = 0, T_before = 0;    // of the latest plan; thresholds of ps and the pair before
+    // Plan of step j (called for every step in turn): split pair, kCorr when some
+    // score needs a correction, and plo << 16.
+    auto plan_step = [&](int j) -> int {
+      const int d_min = nearest(j);
+      advance(low, d_min);
+      advance(far, max(q0 + (p.tile_tokens >> 1) - (KT * (top - j) + KT / 2), 0) + 32);
+      const int ps = low.pair >= P ? P : min(max(far.pair, low.pair), P - (G8 ? 8 : 1));
+      if (ps != ps_now || j == j0) {
+        T_ps = ps < P ? sT[ps] : 0x7FFFFFFF;
+        T_before = ps > 0 ? sT[ps - 1] : -1;
+        ps_now = ps;
+      }
+      const bool corr = low.pair < P && (q1 - KT * (top - j) > T_ps || (ps > low.pair && d_min <= T_before));
+      return ps | (corr ? kCorr : 0) | low.pair << 16;
+    };
     // Copy of Q's unit of 16 pairs that starts the contraction for split pair
     // ps, its pairs below ps zeroed.  The split pair only moves forward and
     // mostly stays put, so an unchanged copy is kept.
@@ -444,64 +524,35 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       fence_proxy_async_smem();
     };
 
-    // this tile's steps: every `stride`-th from j0 on
-    const int stride = dup ? 2 : 1;
-    const int j0 = dup ? t : top - my_last;
-    int plo_next = 0, psr = 0, ps_next = 0;
-    auto plan = [&](int j) {
-      advance_plo(t, top - j, plo_next);
-      ps_next = split_pair(t, top - j, plo_next, psr);
-    };
+    int plan = 0;
     if (j0 < steps) {
-      plan(j0);
-      write_masked_q(ps_next);
+      plan = plan_step(j0);
+      write_masked_q(plan & 0xFF);
+      if (r == 0) sPS[t] = plan & 0xFFFF;
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(q_ready(t));
 
-    int sk = 0, pk = 0;
-    auto next_stage = [&]() {
-      if (++sk == nsk) { sk = 0; pk ^= 1; }
-    };
-    // key tiles that only the other row tile attends: release them
-    for (int j = 0; ok && j < min(j0, steps); ++j) {
-      if (!dup) {
-        // wait for the stage's fill, so that the arrival counts towards this phase
-        if (!__all_sync(FULL, mbar_wait(k_full(sk), pk))) { ok = false; break; }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_empty(sk));
-      }
-      next_stage();
-    }
-
-    for (int j = j0; ok && j < steps; j += stride) {
-      const int kt = top - j;
-      const int kp0 = 128 * kt;
+    const uint32_t tS = lane_base + t * KT;
+    const float sl = p.scale_log2;
+    // Step j, its scores in S: from there to P's hand-over.  Most steps are plain:
+    // no correction, no key masked, not every pair pruned.  They have code of
+    // their own, in one piece; with the other cases' branches in it the
+    // same step took 800 cycles more.
+    auto step = [&](auto is_special, int j, int plan, int plan_next, bool more) {
+      constexpr bool SPECIAL = decltype(is_special)::value;
+      const int kp0 = KT * (top - j);
       const int d_row = i_pos - kp0;           // distance to the tile's first key
-      const int plo = plo_next, ps = ps_next;
-      const bool all_pruned = plo >= P;
-      const bool more = j + stride < steps;
-      if (more) plan(j + stride);
-
       // Per-element corrections, d = d_row - c for column c of the tile:
       // pairs plo .. ps - 1 were left out: add them where 0 <= d <= T;
       // pairs ps .. P - 1 were contracted: subtract them where d > T.
-      const bool need_sub = !all_pruned && __any_sync(FULL, d_row > sT[ps]);
-      const bool need_add = !all_pruned && ps > plo && __any_sync(FULL, d_row >= 0 && d_row - 127 <= sT[ps - 1]);
-      const bool corr = need_sub || need_add;
-      const uint32_t kb = sbase + L::OFF_K + sk * TILE;
-      const uint32_t stage_empty = k_empty(sk);
-      // waiting for the fill first makes the release below count towards this phase
-      if (!__all_sync(FULL, mbar_wait(k_full(sk), pk))) { ok = false; break; }
-      next_stage();
-      if (dup) next_stage();
-      if (!corr) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(stage_empty);
-      }
-      if (!__all_sync(FULL, mbar_wait_handoff(s_full(t), cnt & 1))) { ok = false; break; }
-      tc_fence_after();
-      if (corr) {
+      const int plo = plan >> 16, ps = plan & 0xFF;
+      if (SPECIAL && (plan & kCorr)) {
+        const int sk = j % NSK;
+        const uint32_t kb = sbase + L::OFF_K + sk * TILE;
+        const bool need_sub = __any_sync(FULL, d_row > sT[min(ps, P - 1)]);
+        const int T_add = ps > plo ? sT[ps - 1] : -1;
+        const bool need_add = ps > plo && __any_sync(FULL, d_row >= 0 && d_row - (KT - 1) <= T_add);
         // The products of a group of 8 pairs (or of one pair: its group's with
         // the other pairs' Q elements zeroed) for this warp's 32 rows by
         // warp-level MMAs, m16n8k16: A = Q rows, dims 8 grp .. then P + 8 grp
@@ -567,19 +618,19 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         if constexpr (G8) {
           // whole groups of 8 pairs share a threshold
 #pragma unroll 1
-          for (int gp = plo; gp < P; gp += 8) {
+          for (int gp = min(plo, ps); gp < P; gp += 8) {
             const bool sub = gp >= ps;
             const int T = sT[gp];
             // columns of this row that take the group's term
             const int c_lo = sub || T >= d_row ? 0 : d_row - T;
-            const int c_hi = !sub ? min(d_row, 127) : d_row > T ? min(d_row - T - 1, 127) : -1;
+            const int c_hi = !sub ? min(d_row, KT - 1) : d_row > T ? min(d_row - T - 1, KT - 1) : -1;
             if (!__any_sync(FULL, c_lo <= c_hi)) {
               if (sub) break;                  // later groups are pruned at even fewer columns
               continue;
             }
             load_a(gp >> 3);
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
+            for (int cc = 0; cc < KT / 32; ++cc) {
               const int lo = c_lo - 32 * cc, hi = c_hi - 32 * cc;
               if (!__any_sync(FULL, lo <= 31 && hi >= 0 && lo <= hi)) continue;
               float v[32];
@@ -590,9 +641,8 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             }
           }
         } else {
-          const int T_lo = ps > plo ? sT[ps - 1] : 0;
 #pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
+          for (int cc = 0; cc < KT / 32; ++cc) {
             const int dc = d_row - 32 * cc;                  // distance at the chunk's first column
             const int dmax = __shfl_sync(FULL, dc, 31);      // largest and smallest of the block
             const int dmin = max(__shfl_sync(FULL, dc, 0) - 31, 0);
@@ -601,7 +651,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             int pb = ps, pa = ps;
             if (need_sub)
               while (pb < P && sT[pb] < dmax) ++pb;
-            if (need_add && T_lo >= dmin)
+            if (need_add && T_add >= dmin)
               while (pa > plo && sT[pa - 1] >= dmin) --pa;
             if (pa >= pb) continue;
             float v[32];
@@ -625,29 +675,31 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           }
         }
         tmem_st_wait();
+        // the group's last warp to be through with K releases it
+        __threadfence_block();
         __syncwarp();
-        if (lane == 0) mbar_arrive(stage_empty);
+        if (lane == 0 && (atomicAdd(reinterpret_cast<int*>(smem + L::OFF_LEFT) + t, 1) & 3) == 3)
+          mbar_arrive(k_empty(sk));
       }
-      float sc[128];
+      float sc[KT];
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, &sc[32 * cc]);
+      for (int cc = 0; cc < KT / 32; ++cc) tmem_ld32(tS + 32 * cc, &sc[32 * cc]);
       tmem_ld_wait();
       // the loaded values are only defined after the wait: keep every use below it
 #pragma unroll
-      for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(sc[c]));
-      if (all_pruned) {
+      for (int c = 0; c < KT; ++c) asm volatile("" : "+f"(sc[c]));
+      if (SPECIAL && plo >= P) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) sc[c] = 0.f;   // every pair pruned: score 0
+        for (int c = 0; c < KT; ++c) sc[c] = 0.f;   // every pair pruned: score 0
       }
       // causal mask (d < 0) and the sequence's end: columns c > cm
-      if (q_first(t) - (kp0 + 127) < 0 || kp0 + 128 > it.kv_len) {
-        const int cm = min(max(min(d_row, it.kv_len - 1 - kp0), -1), 128);
+      if (SPECIAL) {
+        const int cm = min(max(min(d_row, it.kv_len - 1 - kp0), -1), KT);
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
+        for (int c = 0; c < KT; ++c)
           if (c > cm) sc[c] = -INFINITY;
       }
       // row max, then the exponentials against the (lazily moved) reference
-      const float sl = p.scale_log2;
       float mt;
       {
         float a16[16], b6[6];
@@ -660,8 +712,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         b6[5] = a16[15];
         mt = fmaxf(max3(b6[0], b6[1], b6[2]), max3(b6[3], b6[4], b6[5])) * sl;
       }
-      // the reference moves only when the max grew by more than 8 (x256);
-      // s_full implies that this tile's previous PV has completed
+      // the reference moves only when the max grew by more than 8 (x256)
       float f = 1.f;
       if (cnt == 0) {
         m_ref = mt;
@@ -669,48 +720,82 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         f = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - mt);
         m_ref = mt;
       }
-      if (cnt > 0 && __any_sync(FULL, f != 1.f)) {
-#pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) {
-          float o[32];
-          tmem_ld32(tO + 32 * cc, o);
+      // (s_full says that this tile's previous PV has left O)
+      const bool scale_o = cnt > 0 && __any_sync(FULL, f != 1.f);
+      if (scale_o) {
+#pragma unroll 1
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t o[16];
+          tmem_ld16u(tO + 16 * cc, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f;
-          tmem_st32(tO + 32 * cc, o);
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st16u(tO + 16 * cc, o);
         }
       }
-      uint32_t pk2[64];                        // p, rounded to bf16 (the MMA's operand type); l sums them unrounded
+      // p, rounded to bf16 (the MMA's operand type), over the first half of S; l sums
+      // them unrounded.  Each half is handed over when it is there.
       {
-        const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+        // Warps w and w + 4 share an SM partition and its exponentials: they take turns
+        // (tile 0 first when both come at once), so that one's products run under
+        // the other's exponentials.  Side by side both would wait for both.  The
+        // wait is short and may be given up: it orders nothing.
+#pragma unroll 1
+        for (int i = 0; i < 64 && busy[warp ^ 4]; ++i) {}
+        if (lane == 0) busy[warp] = 1;
+        if (t == 1 && busy[warp ^ 4]) {
+          if (lane == 0) busy[warp] = 0;
+#pragma unroll 1
+          for (int i = 0; i < 64 && busy[warp ^ 4]; ++i) {}
+          if (lane == 0) busy[warp] = 1;
+        }
+        asm volatile("" : "+f"(nm));           // no exponential above this
         float acc[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          float x0, x1;
-          fma2(x0, x1, sc[2 * i], sc[2 * i + 1], sl, sl, nm, nm);
-          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-          add2(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], acc[2 * (i & 3)], acc[2 * (i & 3) + 1], e0, e1);
-          pk2[i] = pack_bf16x2(e0, e1);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk2[KT / 4];
+#pragma unroll
+          for (int i = 0; i < KT / 4; ++i) {
+            const int c = half * KT / 2 + 2 * i;
+            float x0, x1;
+            fma2(x0, x1, sc[c], sc[c + 1], sl, sl, nm, nm);
+            const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+            add2(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], acc[2 * (i & 3)], acc[2 * (i & 3) + 1], e0, e1);
+            pk2[i] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32u(tS + half * KT / 4, pk2);
+          if (half && lane == 0) busy[warp] = 0;
+          if (!half && more) {                 // before the MMA warp is told of the step
+            write_masked_q(plan_next & 0xFF);
+            if (r == 0) sPS[t] = plan_next & 0xFFFF;
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(half ? p_full(t) : p_half(t));
         }
         l_run = l_run * f + (((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
       }
-      tmem_st32u(tS, &pk2[0]);                 // P overwrites the first 64 columns of S
-      tmem_st32u(tS + 32, &pk2[32]);
-      if (more) write_masked_q(ps_next);       // before P is released to the MMA warp
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(t));
+    };
+    for (int j = j0; ok && j < steps; j += stride) {
+      const bool more = j + stride < steps;
+      const int plan_next = more ? plan_step(j + stride) : 0;
+      const bool special = (plan & kCorr) || (plan >> 16) >= P || nearest(j) < 0 || KT * (top - j + 1) > it.kv_len;
+      if (!__all_sync(FULL, mbar_wait_handoff(s_full(t), cnt & 1))) { ok = false; break; }
+      tc_fence_after();
+      if (special) step(std::true_type{}, j, plan, plan_next, more);
+      else step(std::false_type{}, j, plan, plan_next, more);
       ++cnt;
+      plan = plan_next;
     }
 
     // ----------------------------------------------------------- epilogue
-    if (steps > 0) {                           // every MMA of both tiles has completed
-      (void)__all_sync(FULL, mbar_wait(o_final(t), 0));
-      tc_fence_after();
-    }
+    (void)__all_sync(FULL, mbar_wait(o_final(t), 0));     // this tile's products have completed
+    if (dup) (void)__all_sync(FULL, mbar_wait(o_final(t ^ 1), 0));   // and so has all use of the ring
+    tc_fence_after();
     const bool split = it.parts > 1;
     // dup: group 1 hands its half over through the ring, which every MMA has left
     float* half = reinterpret_cast<float*>(smem);            // [D][128 rows]
@@ -787,7 +872,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == W_MMA) tmem_dealloc(tmem, 512);
+  if (warp == W_MMA) tmem_dealloc(*tmem_slot, 512);
 }
 
 // Merge of the parts of one row block: with w_s = 2^(l_s - max l), out = sum_s

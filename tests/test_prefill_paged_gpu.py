@@ -31,6 +31,8 @@ CASES = {
     "group_65": (64, 8, 1.0, 1e6, 65, 1, 16, [6], [260]),
     "tile_edges": (128, 1, 1.0, 5e5, 3, 3, 128, [128, 256, 129, 127], [128, 256, 257, 383]),
     "mixed_batch": (64, 8, 1.0, 1e6, 14, 2, 16, [1, 200, 1, 1, 37, 1, 90], [900, 1200, 5, 128, 37, 640, 91]),
+    "many_single_tokens": (128, 1, 1.0, 5e5, 8, 4, 16, [1] * 40, [2048 - 7 * i for i in range(40)]),
+    "many_drafts": (64, 8, 1.0, 1e6, 8, 2, 32, [3] * 80, [1500 - 11 * i for i in range(80)]),
     "long_context": (64, 1, 1.0, 1e6, 4, 2, 16, [2, 1], [20000, 9001]),
     "long_context_chunk": (128, 8, 1.0, 1e7, 7, 1, 64, [150], [12000]),
 }
