@@ -151,8 +151,8 @@ struct PagedSmem {
   static constexpr int OFF_LEFT = OFF_PS + 4 * 4;    // warps of each softmax group that left a corrected K tile
   static constexpr int OFF_BUSY = OFF_LEFT + 4 * 4;  // softmax warps at their exponentials
   static constexpr int OFF_BAR = OFF_BUSY + 8 * 4;
-  // k_full, k_empty [NSK], v_full, v_empty [NSV], s_full, p_half, p_full, o_final, q_ready [2], v_fix
-  static constexpr int NBAR = 2 * NSK + 2 * NSV + 11;
+  // k_full, k_empty [NSK], v_full, v_empty [NSV], s_full, p_most, p_full, o_final, q_ready, s_left, pv_done [2], v_fix
+  static constexpr int NBAR = 2 * NSK + 2 * NSV + 15;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_TMEM + 16;
 };
@@ -208,7 +208,11 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   constexpr int KT = L::KT, NSK = L::NSK, NSV = L::NSV, TILE = L::TILE, COL = L::COL;
   constexpr int W_PROD_K = 8, W_MMA = 9, W_PROD_V = 11;   // W_MMA + t issues tile t's products
   constexpr uint32_t TMEM_O = 256;
-  constexpr int kCorr = 1 << 8;         // of a step's plan (split pair + this): scores need corrections
+  // D = 64 leaves 128 TMEM columns free: P has columns of its own, and the next
+  // QK starts as soon as the softmax group has its scores in registers
+  constexpr bool EARLY = D == 64;
+  constexpr int kMost = KT * 3 / 4;     // keys of P's first hand-over
+  constexpr int kCorr = 1 << 8, kSpecial = 1 << 9;   // of a step's plan, beside its split pair
   constexpr uint32_t FULL = 0xffffffffu;
 
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -220,11 +224,13 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   auto v_empty = [&](int s) { return bar + 8 * (2 * NSK + NSV + s); };
   constexpr int B0 = 2 * NSK + 2 * NSV;
   auto s_full = [&](int t) { return bar + 8 * (B0 + t); };
-  auto p_half = [&](int t) { return bar + 8 * (B0 + 2 + t); };
+  auto p_most = [&](int t) { return bar + 8 * (B0 + 2 + t); };
   auto p_full = [&](int t) { return bar + 8 * (B0 + 4 + t); };
   auto o_final = [&](int t) { return bar + 8 * (B0 + 6 + t); };
   auto q_ready = [&](int t) { return bar + 8 * (B0 + 8 + t); };
-  const uint32_t v_fix = bar + 8 * (B0 + 10);
+  auto s_left = [&](int t) { return bar + 8 * (B0 + 10 + t); };
+  auto pv_done = [&](int t) { return bar + 8 * (B0 + 12 + t); };
+  const uint32_t v_fix = bar + 8 * (B0 + 14);
   int* sT = reinterpret_cast<int*>(smem + L::OFF_T);
   volatile int* sPS = reinterpret_cast<volatile int*>(smem + L::OFF_PS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM);
@@ -267,8 +273,10 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 1);
-      mbar_init(p_half(t), 4);
+      mbar_init(p_most(t), 4);
       mbar_init(p_full(t), 4);
+      mbar_init(s_left(t), 4);
+      mbar_init(pv_done(t), 1);
       mbar_init(o_final(t), 1);
       mbar_init(q_ready(t), 4);
     }
@@ -397,7 +405,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           }
         }
         warp_commit(leader, s_full(t));
-        if (plan < kCorr) warp_commit(leader, k_empty(sk));   // else the softmax group still reads K
+        if (!(plan & kCorr)) warp_commit(leader, k_empty(sk));   // else the softmax group still reads K
         step_k();
         if (dup) step_k();
       };
@@ -407,24 +415,34 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         prepare_qk();
         if (ok) issue_qk();
       }
+      const uint32_t tP = EARLY ? TMEM_O + 2 * D + t * (KT / 2) : t * KT;
       for (int n = 0; ok && n < mine; ++n) {
+        const bool more = n + 1 < mine;
+        if (EARLY && more) {
+          ok = __all_sync(FULL, mbar_wait_handoff(s_left(t), n & 1));
+          tc_fence_after();
+          prepare_qk();
+          if (!ok) break;
+          issue_qk();
+        }
         ok = __all_sync(FULL, mbar_wait_handoff(v_full(sv), pv));
         if (tail && n == 0 && j0 == 0) ok = ok && __all_sync(FULL, mbar_wait(v_fix, 0));
         const uint32_t va = v_lo | ((sbase + L::OFF_V + sv * TILE) >> 4);
-        // P comes in two halves: the first one's product runs under the second's exponentials
+        // most of P's product runs under its last exponentials
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && __all_sync(FULL, mbar_wait_handoff(half ? p_full(t) : p_half(t), n & 1));
+        for (int last = 0; last < 2; ++last) {
+          ok = ok && __all_sync(FULL, mbar_wait_handoff(last ? p_full(t) : p_most(t), n & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int ks = half * KT / 32; ks < (half + 1) * KT / 32; ++ks)
-            warp_mma_ts(leader, TMEM_O + t * D, t * KT + ks * 8, va + ((ks * 2 * L::GROUP) >> 4), kv_hi, idesc_pv,
+          for (int ks = last ? kMost / 16 : 0; ks < (last ? KT : kMost) / 16; ++ks)
+            warp_mma_ts(leader, TMEM_O + t * D, tP + ks * 8, va + ((ks * 2 * L::GROUP) >> 4), kv_hi, idesc_pv,
                         (n > 0 || ks > 0) ? 1u : 0u);
-          if (half == 0 && n + 1 < mine) prepare_qk();
+          if (!EARLY && !last && more) prepare_qk();
         }
         if (!ok) break;
-        if (n + 1 < mine) issue_qk();          // first: the softmax group waits for it
+        if (EARLY) warp_commit(leader, pv_done(t));
+        else if (more) issue_qk();             // first: the softmax group waits for it
         warp_commit(leader, v_empty(sv));
         step_v();
         if (dup) step_v();
@@ -487,20 +505,29 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     const int j0 = dup ? t : top - my_last;
     Cursor low{0, sT[0]}, far = low;
     int ps_now = P, T_ps = 0, T_before = 0;    // of the latest plan; thresholds of ps and the pair before
-    // Plan of step j (called for every step in turn): split pair, kCorr when some
-    // score needs a correction, and plo << 16.
+    int quiet = 0;                             // steps behind the latest planned one that have the same plan
+    // Plan of step j (called for steps in turn): split pair, kCorr when some score
+    // needs a correction, kSpecial when anything but the plain step is to be
+    // done, and plo << 16.  From one step to the next all distances grow by
+    // the same amount, so a plain plan holds until the first of three
+    // thresholds is passed.
     auto plan_step = [&](int j) -> int {
-      const int d_min = nearest(j);
+      const int kp0 = KT * (top - j), d_min = nearest(j);
       advance(low, d_min);
-      advance(far, max(q0 + (p.tile_tokens >> 1) - (KT * (top - j) + KT / 2), 0) + 32);
+      const int centre = max(q0 + (p.tile_tokens >> 1) - (kp0 + KT / 2), 0) + 32;
+      advance(far, centre);
       const int ps = low.pair >= P ? P : min(max(far.pair, low.pair), P - (G8 ? 8 : 1));
       if (ps != ps_now || j == j0) {
         T_ps = ps < P ? sT[ps] : 0x7FFFFFFF;
         T_before = ps > 0 ? sT[ps - 1] : -1;
         ps_now = ps;
       }
-      const bool corr = low.pair < P && (q1 - KT * (top - j) > T_ps || (ps > low.pair && d_min <= T_before));
-      return ps | (corr ? kCorr : 0) | low.pair << 16;
+      const bool corr = low.pair < P && (q1 - kp0 > T_ps || (ps > low.pair && d_min <= T_before));
+      const bool special = corr || low.pair >= P || d_min < 0 || kp0 + KT > it.kv_len;
+      const int shift = dup ? 8 : 7;
+      static_assert(KT == 128, "steps are 128 keys, or 256, apart");
+      quiet = special ? 0 : min(min(low.T - d_min, far.T - centre), T_ps - (q1 - kp0)) >> shift;
+      return ps | (corr ? kCorr : 0) | (special ? kSpecial : 0) | low.pair << 16;
     };
     // Copy of Q's unit of 16 pairs that starts the contraction for split pair
     // ps, its pairs below ps zeroed.  The split pair only moves forward and
@@ -533,7 +560,13 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     __syncwarp();
     if (lane == 0) mbar_arrive(q_ready(t));
 
-    const uint32_t tS = lane_base + t * KT;
+    const uint32_t tS = lane_base + t * KT, tP = EARLY ? lane_base + TMEM_O + 2 * D + t * (KT / 2) : tS;
+    // what the MMA warp needs for the next QK, before the arrival that lets it start
+    auto tell_next = [&](int plan, int plan_next) {
+      if (plan_next == plan) return;
+      write_masked_q(plan_next & 0xFF);
+      if (r == 0) sPS[t] = plan_next & 0xFFFF;
+    };
     const float sl = p.scale_log2;
     // Step j, its scores in S: from there to P's hand-over.  Most steps are plain:
     // no correction, no key masked, not every pair pruned.  They have code of
@@ -685,6 +718,12 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
       for (int cc = 0; cc < KT / 32; ++cc) tmem_ld32(tS + 32 * cc, &sc[32 * cc]);
       tmem_ld_wait();
+      if (EARLY) {                             // S may be overwritten
+        if (more) tell_next(plan, plan_next);
+        tc_fence_before();
+        __syncwarp();
+        if (more && lane == 0) mbar_arrive(s_left(t));
+      }
       // the loaded values are only defined after the wait: keep every use below it
 #pragma unroll
       for (int c = 0; c < KT; ++c) asm volatile("" : "+f"(sc[c]));
@@ -720,8 +759,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         f = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - mt);
         m_ref = mt;
       }
-      // (s_full says that this tile's previous PV has left O)
+      // this tile's previous PV has left O (and P) once s_full, or pv_done, says so
       const bool scale_o = cnt > 0 && __any_sync(FULL, f != 1.f);
+      if (EARLY && cnt > 0) (void)__all_sync(FULL, mbar_wait_handoff(pv_done(t), (cnt - 1) & 1));
       if (scale_o) {
 #pragma unroll 1
         for (int cc = 0; cc < D / 16; ++cc) {
@@ -733,8 +773,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           tmem_st16u(tO + 16 * cc, o);
         }
       }
-      // p, rounded to bf16 (the MMA's operand type), over the first half of S; l sums
-      // them unrounded.  Each half is handed over when it is there.
+      // p, rounded to bf16 (the MMA's operand type); l sums them unrounded
       {
         float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
         // Warps w and w + 4 share an SM partition and its exponentials: they take turns
@@ -754,39 +793,41 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         float acc[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+        uint32_t pk2[KT / 2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk2[KT / 4];
-#pragma unroll
-          for (int i = 0; i < KT / 4; ++i) {
-            const int c = half * KT / 2 + 2 * i;
-            float x0, x1;
-            fma2(x0, x1, sc[c], sc[c + 1], sl, sl, nm, nm);
-            const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-            add2(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], acc[2 * (i & 3)], acc[2 * (i & 3) + 1], e0, e1);
-            pk2[i] = pack_bf16x2(e0, e1);
+        for (int i = 0; i < KT / 2; ++i) {
+          float x0, x1;
+          fma2(x0, x1, sc[2 * i], sc[2 * i + 1], sl, sl, nm, nm);
+          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+          add2(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], acc[2 * (i & 3)], acc[2 * (i & 3) + 1], e0, e1);
+          pk2[i] = pack_bf16x2(e0, e1);
+          if (i == kMost / 2 - 1) {
+            tmem_st32u(tP, pk2);
+            tmem_st16u(tP + 32, pk2 + 32);
+            if (!EARLY && more) tell_next(plan, plan_next);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_most(t));
           }
-          tmem_st32u(tS + half * KT / 4, pk2);
-          if (half && lane == 0) busy[warp] = 0;
-          if (!half && more) {                 // before the MMA warp is told of the step
-            write_masked_q(plan_next & 0xFF);
-            if (r == 0) sPS[t] = plan_next & 0xFFFF;
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(half ? p_full(t) : p_half(t));
         }
+        tmem_st16u(tP + 48, pk2 + 48);
+        if (lane == 0) busy[warp] = 0;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
         l_run = l_run * f + (((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
       }
     };
     for (int j = j0; ok && j < steps; j += stride) {
       const bool more = j + stride < steps;
-      const int plan_next = more ? plan_step(j + stride) : 0;
-      const bool special = (plan & kCorr) || (plan >> 16) >= P || nearest(j) < 0 || KT * (top - j + 1) > it.kv_len;
+      int plan_next = plan;
+      if (quiet > 0) --quiet;
+      else if (more) plan_next = plan_step(j + stride);
       if (!__all_sync(FULL, mbar_wait_handoff(s_full(t), cnt & 1))) { ok = false; break; }
       tc_fence_after();
-      if (special) step(std::true_type{}, j, plan, plan_next, more);
+      if (plan & kSpecial) step(std::true_type{}, j, plan, plan_next, more);
       else step(std::false_type{}, j, plan, plan_next, more);
       ++cnt;
       plan = plan_next;
