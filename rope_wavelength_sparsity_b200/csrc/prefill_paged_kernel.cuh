@@ -145,8 +145,7 @@ struct PagedSmem {
   static constexpr int OFF_Q1 = OFF_K + NSK * TILE;
   static constexpr int OFF_Q0 = OFF_Q1 + 128 * D * 2;
   static constexpr int OFF_QM = OFF_Q0 + 128 * D * 2;    // per tile: Q's first unit with its left-out pairs zeroed
-  static constexpr int OFF_SCR = OFF_QM + 2 * 4 * COL;   // per warp [32 rows][16 keys] fp32
-  static constexpr int OFF_T = OFF_SCR + 8 * 2048;
+  static constexpr int OFF_T = OFF_QM + 2 * 4 * COL;
   static constexpr int OFF_PS = OFF_T + 64 * 4;      // plan of each tile's next step
   static constexpr int OFF_LEFT = OFF_PS + 4 * 4;    // warps of each softmax group that left a corrected K tile
   static constexpr int OFF_BUSY = OFF_LEFT + 4 * 4;  // softmax warps at their exponentials
@@ -158,6 +157,25 @@ struct PagedSmem {
 };
 static_assert(PagedSmem<64>::NSK % 2 == 0 && PagedSmem<128>::NSK % 2 == 0, "even rings");
 static_assert(PagedSmem<128>::ALLOC <= 232448 && PagedSmem<64>::ALLOC <= 232448, "shared memory of one CTA");
+
+// 32 columns of 16 TMEM lanes in the layout of four m16n8 MMA accumulators: register
+// 4 i + e is row lane / 4 + 8 (e >> 1), column 8 i + 2 (lane % 4) + (e & 1).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&u)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&u)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
 
 // True in one lane of a converged warp.
 __device__ __forceinline__ uint32_t elect_one() {
@@ -586,126 +604,87 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const bool need_sub = __any_sync(FULL, d_row > sT[min(ps, P - 1)]);
         const int T_add = ps > plo ? sT[ps - 1] : -1;
         const bool need_add = ps > plo && __any_sync(FULL, d_row >= 0 && d_row - (KT - 1) <= T_add);
-        // The products of a group of 8 pairs (or of one pair: its group's with
-        // the other pairs' Q elements zeroed) for this warp's 32 rows by
-        // warp-level MMAs, m16n8k16: A = Q rows, dims 8 grp .. then P + 8 grp
-        // .., B = K rows; a per-warp scratch turns them into one row per lane.
-        float* scr = reinterpret_cast<float*>(smem + L::OFF_SCR) + warp * 512;   // [32 rows][16 keys]
+        // A pair's (g = 8: a group's) products for this warp's 32 rows by warp-level
+        // MMAs, m16n8k16: A = Q rows, dims 8 grp .. then P + 8 grp .. (a lane's
+        // register halves are pairs 8 grp + 2 (lane & 3) (+ 1), all but the pair's
+        // own zeroed), B = K rows.  S comes from TMEM in the layout of their
+        // accumulators (16 lanes x 256 bits), is their addend, and every element
+        // chooses by its distance.  (Through a scratch and row by row a pair took
+        // 450 cycles for 32 keys.)
         const int qm = lane >> 3, qi = lane & 7;
-        uint32_t afr[2][4];
-        auto load_a = [&](int grp) {           // matrix m: rows 8 (m & 1) .., half m >> 1
+        int pr[4];                             // distances of this lane's rows 8 k + lane / 4 to the tile's first key
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            const int row_a = wq * 32 + 16 * mt + 8 * (qm & 1) + qi;
-            const int col = (qm >> 1) ? P / 8 + grp : grp;
-            ldsm_x4(smem_u32(smem_q) + col * COL + row_a * 16, afr[mt][0], afr[mt][1], afr[mt][2], afr[mt][3]);
-          }
-        };
-        // v[c] += sgn * product, for this row's columns lo .. hi of chunk cc
-        auto apply = [&](float (&v)[32], int cc, int grp, uint32_t keep, int lo, int hi, float sgn) {
+        for (int k = 0; k < 4; ++k) pr[k] = __shfl_sync(FULL, d_row, (lane >> 2) + 8 * k) - 2 * (lane & 3);
+        int d_first[2], d_last[2];             // of 16 rows
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            // B: matrix m = keys 8 (m >> 1) .., first (m even) or second half of the group
-            const int key = 32 * cc + 16 * half + 8 * (qm >> 1) + qi;
-            const int ch = (qm & 1) ? P / 8 + grp : grp;
-            uint32_t b00, b01, b10, b11;
-            ldsm_x4(kb + (key >> 3) * L::GROUP + (ch >> 3) * 1024 + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
-                    b00, b01, b10, b11);
-            float acc[2][2][4];
+        for (int mt = 0; mt < 2; ++mt) {
+          d_first[mt] = __shfl_sync(FULL, d_row, 16 * mt);
+          d_last[mt] = __shfl_sync(FULL, d_row, 16 * mt + 15);
+        }
+#pragma unroll 1
+        for (int cc = 0; cc < KT / 32; ++cc) {
+          const int dmax = d_last[1] - 32 * cc, dmin = max(d_first[0] - 32 * cc - 31, 0);
+          if (dmax < 0) continue;              // wholly acausal
+          // pairs ps .. pb - 1 are pruned somewhere in the chunk, pa .. ps - 1 kept somewhere
+          int pb = ps, pa = ps;
+          if (need_sub)
+            while (pb < P && sT[pb] < dmax) ++pb;
+          if (need_add && T_add >= dmin)
+            while (pa > plo && sT[pa - 1] >= dmin) --pa;
+          if (pa >= pb) continue;
+          uint32_t v[2][16];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < 2; ++mt) tmem_ld_frag(tS + 32 * cc + (static_cast<uint32_t>(16 * mt) << 16), v[mt]);
+          tmem_ld_wait();
+          uint32_t af[2][4], bf[4][2];
+          int cur = -1;
+#pragma unroll 1
+          for (int pp = pa; pp < pb; pp += G8 ? 8 : 1) {
+            const int grp = pp >> 3;
+            if (grp != cur) {
+              cur = grp;
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt)
+              for (int mt = 0; mt < 2; ++mt)   // matrix m: rows 8 (m & 1) .., half m >> 1
+                ldsm_x4(smem_u32(smem_q) + ((qm >> 1) ? P / 8 + grp : grp) * COL + (wq * 32 + 16 * mt + 8 * (qm & 1) + qi) * 16,
+                        af[mt][0], af[mt][1], af[mt][2], af[mt][3]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
+              for (int hp = 0; hp < 2; ++hp) { // matrix m: keys 8 (m >> 1) .., first (m even) or second half
+                const int key = 32 * cc + 16 * hp + 8 * (qm >> 1) + qi;
+                const int ch = (qm & 1) ? P / 8 + grp : grp;
+                ldsm_x4(kb + (key >> 3) * L::GROUP + (ch >> 3) * 1024 + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
+                        bf[2 * hp][0], bf[2 * hp][1], bf[2 * hp + 1][0], bf[2 * hp + 1][1]);
+              }
+            }
+            const bool sub = pp >= ps;
+            const uint32_t keep = G8 || (lane & 3) == ((pp & 7) >> 1) ? (G8 ? 0xFFFFFFFFu : (pp & 1) ? 0xFFFF0000u : 0x0000FFFFu)
+                                                                     : 0u;
+            const uint32_t flip = sub ? 0x80008000u & keep : 0u;   // subtract: Q with its sign turned
+            const int edge = 32 * cc + sT[pp];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              const uint32_t a0 = afr[mt][0] & keep, a1 = afr[mt][1] & keep;
-              const uint32_t a2 = afr[mt][2] & keep, a3 = afr[mt][3] & keep;
-              mma_16816_bf16(acc[mt][0], a0, a1, a2, a3, b00, b01);
-              mma_16816_bf16(acc[mt][1], a0, a1, a2, a3, b10, b11);
-            }
-            __syncwarp();                      // the scratch's previous rows have been read
+              const uint32_t a0 = (af[mt][0] & keep) ^ flip, a1 = (af[mt][1] & keep) ^ flip;
+              const uint32_t a2 = (af[mt][2] & keep) ^ flip, a3 = (af[mt][3] & keep) ^ flip;
+              // columns below d - edge are beyond the threshold: in none of the rows, or in all
+              if (sub ? d_last[mt] <= edge : d_first[mt] - edge >= 32) continue;
+              const int r0 = pr[2 * mt] - edge, r1 = pr[2 * mt + 1] - edge;
+              float z[4][4];
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+              for (int nt = 0; nt < 4; ++nt) {
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt) {
-                const int rr = 16 * mt + (lane >> 2), cl = 8 * nt + 2 * (lane & 3);
-                *reinterpret_cast<float2*>(scr + rr * 16 + cl) = make_float2(acc[mt][nt][0], acc[mt][nt][1]);
-                *reinterpret_cast<float2*>(scr + (rr + 8) * 16 + cl) = make_float2(acc[mt][nt][2], acc[mt][nt][3]);
+                for (int e = 0; e < 4; ++e) z[nt][e] = __uint_as_float(v[mt][4 * nt + e]);
+                mma_16816_bf16(z[nt], a0, a1, a2, a3, bf[nt][0], bf[nt][1]);
               }
-            __syncwarp();
-            const float4* mine = reinterpret_cast<const float4*>(scr + lane * 16);
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-              const float4 x = mine[c4];
-              const float xs[4] = {x.x, x.y, x.z, x.w};
+              for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int c = 16 * half + 4 * c4 + e;
-                if (c >= lo && c <= hi) v[c] = fmaf(sgn, xs[e], v[c]);
-              }
+                for (int e = 0; e < 4; ++e) {
+                  const bool beyond = 8 * nt + (e & 1) < (e < 2 ? r0 : r1);
+                  v[mt][4 * nt + e] = beyond == sub ? __float_as_uint(z[nt][e]) : v[mt][4 * nt + e];
+                }
             }
           }
-        };
-        if constexpr (G8) {
-          // whole groups of 8 pairs share a threshold
-#pragma unroll 1
-          for (int gp = min(plo, ps); gp < P; gp += 8) {
-            const bool sub = gp >= ps;
-            const int T = sT[gp];
-            // columns of this row that take the group's term
-            const int c_lo = sub || T >= d_row ? 0 : d_row - T;
-            const int c_hi = !sub ? min(d_row, KT - 1) : d_row > T ? min(d_row - T - 1, KT - 1) : -1;
-            if (!__any_sync(FULL, c_lo <= c_hi)) {
-              if (sub) break;                  // later groups are pruned at even fewer columns
-              continue;
-            }
-            load_a(gp >> 3);
-#pragma unroll 1
-            for (int cc = 0; cc < KT / 32; ++cc) {
-              const int lo = c_lo - 32 * cc, hi = c_hi - 32 * cc;
-              if (!__any_sync(FULL, lo <= 31 && hi >= 0 && lo <= hi)) continue;
-              float v[32];
-              tmem_ld32(tS + 32 * cc, v);
-              tmem_ld_wait();
-              apply(v, cc, gp >> 3, 0xFFFFFFFFu, lo, hi, sub ? -1.f : 1.f);
-              tmem_st32(tS + 32 * cc, v);
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int cc = 0; cc < KT / 32; ++cc) {
-            const int dc = d_row - 32 * cc;                  // distance at the chunk's first column
-            const int dmax = __shfl_sync(FULL, dc, 31);      // largest and smallest of the block
-            const int dmin = max(__shfl_sync(FULL, dc, 0) - 31, 0);
-            if (dmax < 0) continue;                          // wholly acausal
-            // pairs ps .. pb - 1 are pruned somewhere in the block, pa .. ps - 1 kept somewhere
-            int pb = ps, pa = ps;
-            if (need_sub)
-              while (pb < P && sT[pb] < dmax) ++pb;
-            if (need_add && T_add >= dmin)
-              while (pa > plo && sT[pa - 1] >= dmin) --pa;
-            if (pa >= pb) continue;
-            float v[32];
-            tmem_ld32(tS + 32 * cc, v);
-            tmem_ld_wait();
-            int cur = -1;
-#pragma unroll 1
-            for (int pp = pa; pp < pb; ++pp) {
-              if ((pp >> 3) != cur) load_a(cur = pp >> 3);
-              const int T = sT[pp];
-              const bool sub = pp >= ps;
-              const int lo = sub || T >= dc ? 0 : dc - T;
-              const int hi = !sub ? min(dc, 31) : dc > T ? min(dc - T, 32) - 1 : -1;
-              if (!__any_sync(FULL, lo <= hi)) continue;
-              // a lane's A register halves hold pairs 8 grp + 2 (lane & 3) (+ 1)
-              const int jp = pp & 7;
-              const uint32_t keep = ((lane & 3) == (jp >> 1)) ? ((jp & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-              apply(v, cc, cur, keep, lo, hi, sub ? -1.f : 1.f);
-            }
-            tmem_st32(tS + 32 * cc, v);
-          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) tmem_st_frag(tS + 32 * cc + (static_cast<uint32_t>(16 * mt) << 16), v[mt]);
         }
         tmem_st_wait();
         // the group's last warp to be through with K releases it
