@@ -113,7 +113,7 @@ int64_t sum_lengths(const int32_t* len, int32_t B) {
 // blocks' key ranges are cut into; those with several parts come first.
 struct PagedPlan {
   int n = 0, ctas = 0, split_ctas = 0;
-  uint16_t seq[kPagedMaxB], parts[kPagedMaxB];
+  uint16_t seq[kPagedMaxB], parts[kPagedMaxB], lead[kPagedMaxB];
   int item0[kPagedMaxB + 1];
   size_t bytes(int D) const { return static_cast<size_t>(split_ctas) * 256 * (D + 1) * sizeof(float); }
 };
@@ -147,68 +147,76 @@ float wave_time(const int* count, const float* cost, int n, int slots) {
   return lv[m - 1].t + rest;
 }
 
-// Costs are in steps of a two-tile row block (a tile of 128 keys for both).  A one-tile block's step costs kDupStep of one, a CTA's start and end
-// kCtaSteps, the merge pass kMergeSteps.  The length of a part is the one
-// whose grid these say is done first, out of those that make about 1 .. 12
-// waves of the whole work, and no split at all.
-constexpr float kDupStep = 0.6f, kCtaSteps = 2.5f, kMergeSteps = 2.f;
-constexpr int kMinPartTiles = 3, kMaxParts = 64;
+// Measured costs in microseconds, [row tiles of a block - 1]: a key tile of 128
+// keys (D = 64, 128), a CTA's start and end, each threshold that the walk
+// passes (most lie within kLeadKeys of the diagonal, so the part of the last
+// keys is made shorter by them), and the merge pass.
+constexpr float kTileUs[2][2] = {{0.95f, 1.75f}, {1.4f, 2.1f}};
+constexpr float kCtaUs[2] = {7.f, 10.f}, kPairUs[2] = {0.8f, 1.5f}, kMergeUs = 5.f;
+constexpr int kMinPartTiles = 3, kMaxParts = 64, kLeadKeys = 1024;
 
-bool plan_paged(const int32_t* q_len, const int32_t* kv_len, int B, int G, int Hkv, int D, int num_sms,
-                PagedPlan* out) {
-  (void)D;
+// The length of a part is the one whose grid these costs say is done first, out
+// of some that make a fraction of a wave to a dozen waves of the whole work, and
+// no split at all.
+bool plan_paged(const int32_t* q_len, const int32_t* kv_len, int B, int G, int Hkv, const WindowPlan& window,
+                int num_sms, PagedPlan* out) {
   const int tile_tokens = 128 / G;
-  struct Work { int b, blocks, nkt; float step; };
+  struct Work { int b, blocks, nkt, lead; float tile, us, cta; };
   Work w[kPagedMaxB];
-  int n = 0, longest = 0;
+  int n = 0;
   double total = 0;
   for (int b = 0; b < B; ++b) {
     if (q_len[b] == 0) continue;
-    const int tiles = (q_len[b] + tile_tokens - 1) / tile_tokens;
-    w[n] = Work{b, (tiles + 1) / 2, (kv_len[b] + 127) / 128, tiles > 1 ? 1.f : kDupStep};
-    total += static_cast<double>(w[n].blocks) * Hkv * w[n].nkt * w[n].step;
-    longest = std::max(longest, w[n].nkt);
-    ++n;
+    const int tiles = (q_len[b] + tile_tokens - 1) / tile_tokens, two = tiles > 1 ? 1 : 0;
+    const float tile = kTileUs[window.D == 128][two];
+    int passed = 0;
+    for (int i = 0; i < window.P; i += window.g)
+      passed += window.T[i] < std::min(kv_len[b], kLeadKeys) ? 1 : 0;
+    Work& x = w[n++];
+    x = Work{b, (tiles + 1) / 2, (kv_len[b] + 127) / 128, static_cast<int>(passed * kPairUs[two] / tile), tile, 0.f,
+             kCtaUs[two]};
+    x.us = (x.nkt + x.lead) * tile;
+    total += static_cast<double>(x.blocks) * Hkv * x.us;
   }
   // longest rows first
-  std::sort(w, w + n, [](const Work& a, const Work& b) {
-    return a.nkt * a.step != b.nkt * b.step ? a.nkt * a.step > b.nkt * b.step : a.b < b.b;
-  });
-  auto parts_of = [&](const Work& x, int len) {   // parts of at most `len` step costs
-    const int tiles = std::max(kMinPartTiles, static_cast<int>(len / x.step));
-    return std::min(kMaxParts, std::max(1, (x.nkt + tiles - 1) / tiles));
+  std::sort(w, w + n, [](const Work& a, const Work& b) { return a.us != b.us ? a.us > b.us : a.b < b.b; });
+  auto parts_of = [&](const Work& x, double us) {   // parts of about `us` each
+    const int tiles = static_cast<int>(std::max<double>(kMinPartTiles, std::min(us / x.tile, 1e9)));
+    const int parts = std::min(kMaxParts, (x.nkt + x.lead + tiles - 1) / tiles);
+    return std::max(1, std::min(parts, x.nkt / kMinPartTiles));
   };
   int count[kPagedMaxB];
   float cost[kPagedMaxB];
-  int best_len = INT32_MAX;
+  double best_us = 1e12;
   float best = 0;
-  for (int k = 0; k <= 12; ++k) {
-    const int len = k == 0 ? INT32_MAX / 2 : static_cast<int>(total / (static_cast<double>(num_sms) * k)) + 1;
-    if (k > 0 && len >= longest) continue;        // nothing would be split
-    if (k > 0 && len < kMinPartTiles) break;
+  constexpr float kWaves[] = {0.f, 0.4f, 0.5f, 0.6f, 0.7f, 0.8f, 0.9f, 1.f, 1.2f, 1.5f, 1.8f, 2.f, 2.5f, 3.f, 4.f, 5.f, 7.f, 9.f, 12.f};
+  for (const float k : kWaves) {
+    const double us = k == 0 ? 1e12 : total / (static_cast<double>(num_sms) * k);
+    if (k > 0 && n > 0 && us >= w[0].us) continue;  // nothing would be split
     int m = 0;
     bool split = false;
     for (int i = 0; i < n; ++i) {
-      const int parts = parts_of(w[i], len);
-      const float c = (w[i].nkt + parts - 1) / parts * w[i].step + kCtaSteps;
+      const int parts = parts_of(w[i], us);
+      const float c = (w[i].nkt + w[i].lead + parts - 1) / parts * w[i].tile + w[i].cta;
       const int64_t ctas = int64_t(w[i].blocks) * Hkv * parts;
       split |= parts > 1;
       if (ctas > INT32_MAX / 2) return false;
       if (m > 0 && cost[m - 1] == c && count[m - 1] < INT32_MAX / 2) count[m - 1] += static_cast<int>(ctas);
       else { cost[m] = c; count[m++] = static_cast<int>(ctas); }
     }
-    const float t = wave_time(count, cost, m, num_sms) + (split ? kMergeSteps : 0.f);
-    if (k == 0 || t < best) { best = t; best_len = len; }
+    const float t = wave_time(count, cost, m, num_sms) + (split ? kMergeUs : 0.f);
+    if (k == 0 || t < best) { best = t; best_us = us; }
   }
   // split sequences first: only their CTAs have room in the workspace
   int64_t ctas = 0;
   out->n = 0;
   for (int pass = 0; pass < 2; ++pass) {
     for (int i = 0; i < n; ++i) {
-      const int parts = parts_of(w[i], best_len);
+      const int parts = parts_of(w[i], best_us);
       if ((parts > 1) != (pass == 0)) continue;
       out->item0[out->n] = static_cast<int>(ctas);
       out->seq[out->n] = static_cast<uint16_t>(w[i].b);
+      out->lead[out->n] = static_cast<uint16_t>(w[i].lead);
       out->parts[out->n++] = static_cast<uint16_t>(parts);
       ctas += int64_t(w[i].blocks) * Hkv * parts;
       if (ctas > INT32_MAX) return false;
@@ -253,6 +261,7 @@ int launch_paged(const PagedCall& c) {
   std::copy(c.plan.item0, c.plan.item0 + c.plan.n + 1, p.item0);
   std::copy(c.plan.seq, c.plan.seq + c.plan.n, p.seq);
   std::copy(c.plan.parts, c.plan.parts + c.plan.n, p.parts);
+  std::copy(c.plan.lead, c.plan.lead + c.plan.n, p.lead);
   for (int b = 0; b < c.B; ++b) {
     p.q_start[b + 1] = p.q_start[b] + c.q_len[b];
     p.kv_len[b] = c.kv_len[b];
@@ -374,7 +383,7 @@ size_t wpattn_prefill_paged_workspace_size(const wpattn_window* w, const int32_t
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != WPATTN_OK) return 0;
   PagedPlan pp;
-  return plan_paged(q_len_host, kv_len_host, B, Hq / Hkv, Hkv, plan.D, dev->num_sms, &pp) ? pp.bytes(plan.D) : 0;
+  return plan_paged(q_len_host, kv_len_host, B, Hq / Hkv, Hkv, plan, dev->num_sms, &pp) ? pp.bytes(plan.D) : 0;
 }
 
 int wpattn_prefill_paged(const wpattn_window* w, const void* q, const void* k_pages, const void* v_pages,
@@ -403,7 +412,7 @@ int wpattn_prefill_paged(const wpattn_window* w, const void* q, const void* k_pa
   if (cap > (int64_t(1) << 30) || int64_t(num_pages) * page_size >= (int64_t(1) << 31)) return WPATTN_EUNSUPPORTED;
   PagedCall c;
   if ((rc = device_info(&c.dev)) != WPATTN_OK) return rc;
-  if (!plan_paged(q_len_host, kv_len_host, B, Hq / Hkv, Hkv, plan.D, c.dev->num_sms, &c.plan))
+  if (!plan_paged(q_len_host, kv_len_host, B, Hq / Hkv, Hkv, plan, c.dev->num_sms, &c.plan))
     return WPATTN_EUNSUPPORTED;
   if (c.plan.split_ctas > 0) {
     if (!workspace || workspace_bytes < c.plan.bytes(plan.D)) return WPATTN_EWORKSPACE;

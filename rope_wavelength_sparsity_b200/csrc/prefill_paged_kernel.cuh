@@ -75,7 +75,8 @@ struct PrefillPagedParams {
   // sequences in the order of the grid: CTA c belongs to the i-th when item0[i] <= c < item0[i + 1]
   int item0[MAXB + 1];
   uint16_t seq[MAXB];
-  uint16_t parts[MAXB];     // key ranges of each of its row blocks
+  uint16_t parts[MAXB];     // key ranges of each of its row blocks,
+  uint16_t lead[MAXB];      // equal but for the one of the last keys, which is this many tiles shorter
   int q_start[MAXB + 1];    // by sequence: first row in q
   int kv_len[MAXB];
 };
@@ -92,7 +93,7 @@ __device__ __forceinline__ int find_sequence(const int* start, int n, int at) {
 
 // What CTA c works on.
 struct PagedItem {
-  int b, kvh, rb, part, parts;
+  int b, kvh, rb, part, parts, lead;
   int q_len, kv_len, row0;  // row0: the sequence's first row in q
   int tok[2], ntok[2];      // first token and tokens of each row tile
   bool dup;
@@ -105,6 +106,7 @@ __device__ __forceinline__ PagedItem paged_item(const PrefillPagedParams<MAXB>& 
   const int local = c - p.item0[i];
   it.b = p.seq[i];
   it.parts = p.parts[i];
+  it.lead = p.lead[i];
   it.row0 = p.q_start[it.b];
   it.q_len = p.q_start[it.b + 1] - it.row0;
   it.kv_len = p.kv_len[it.b];
@@ -262,7 +264,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   const PagedItem it = paged_item(p, blockIdx.x);
   const bool dup = it.dup;
   const int nkt = (it.kv_len + KT - 1) / KT;
-  const int per = (nkt + it.parts - 1) / it.parts;
+  const int per = it.parts > 1 ? (nkt + it.lead + it.parts - 1) / it.parts : nkt;
   const int kt_lo = it.part * per, kt_hi = min(kt_lo + per, nkt) - 1;
   const int pos0 = it.kv_len - it.q_len;              // the chunk's first position
   auto q_first = [&](int t) { return pos0 + (t == 0 ? it.tok[0] : it.tok[1]); };
