@@ -153,7 +153,7 @@ float wave_time(const int* count, const float* cost, int n, int slots) {
 // keys is made shorter by them), and the merge pass.
 constexpr float kTileUs[2][2] = {{0.95f, 1.75f}, {1.4f, 2.1f}};
 constexpr float kCtaUs[2] = {7.f, 10.f}, kPairUs[2] = {0.8f, 1.5f}, kMergeUs = 5.f;
-constexpr int kMinPartTiles = 3, kMaxParts = 64, kLeadKeys = 1024;
+constexpr int kMinPartTiles = 2, kMaxParts = 64, kLeadKeys = 1024;
 
 // The length of a part is the one whose grid these costs say is done first, out
 // of some that make a fraction of a wave to a dozen waves of the whole work, and
@@ -185,6 +185,14 @@ bool plan_paged(const int32_t* q_len, const int32_t* kv_len, int B, int G, int H
     const int parts = std::min(kMaxParts, (x.nkt + x.lead + tiles - 1) / tiles);
     return std::max(1, std::min(parts, x.nkt / kMinPartTiles));
   };
+  // tiles that the last part is shorter by, at most so many that it keeps one
+  auto lead_of = [&](const Work& x, int parts) {
+    return parts < 2 ? 0 : std::max(0, std::min(x.lead, (x.nkt - 1) / (parts - 1) * parts - x.nkt));
+  };
+  auto cta_us = [&](const Work& x, int parts) {   // of a row block's longest part
+    const int per = (x.nkt + lead_of(x, parts) + parts - 1) / parts;
+    return std::max(per, x.nkt - (parts - 1) * per + x.lead) * x.tile + x.cta;
+  };
   int count[kPagedMaxB];
   float cost[kPagedMaxB];
   double best_us = 1e12;
@@ -197,7 +205,7 @@ bool plan_paged(const int32_t* q_len, const int32_t* kv_len, int B, int G, int H
     bool split = false;
     for (int i = 0; i < n; ++i) {
       const int parts = parts_of(w[i], us);
-      const float c = (w[i].nkt + w[i].lead + parts - 1) / parts * w[i].tile + w[i].cta;
+      const float c = cta_us(w[i], parts);
       const int64_t ctas = int64_t(w[i].blocks) * Hkv * parts;
       split |= parts > 1;
       if (ctas > INT32_MAX / 2) return false;
@@ -216,7 +224,7 @@ bool plan_paged(const int32_t* q_len, const int32_t* kv_len, int B, int G, int H
       if ((parts > 1) != (pass == 0)) continue;
       out->item0[out->n] = static_cast<int>(ctas);
       out->seq[out->n] = static_cast<uint16_t>(w[i].b);
-      out->lead[out->n] = static_cast<uint16_t>(w[i].lead);
+      out->lead[out->n] = static_cast<uint16_t>(lead_of(w[i], parts));
       out->parts[out->n++] = static_cast<uint16_t>(parts);
       ctas += int64_t(w[i].blocks) * Hkv * parts;
       if (ctas > INT32_MAX) return false;

@@ -549,6 +549,11 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       quiet = special ? 0 : min(min(low.T - d_min, far.T - centre), T_ps - (q1 - kp0)) >> shift;
       return ps | (corr ? kCorr : 0) | (special ? kSpecial : 0) | low.pair << 16;
     };
+    // pairs whose threshold is below d (thresholds grow; two a lane)
+    const int T_lo = lane < P ? sT[lane] : 0x7FFFFFFF, T_hi = lane + 32 < P ? sT[lane + 32] : 0x7FFFFFFF;
+    auto pairs_below = [&](int d) -> int {
+      return __popc(__ballot_sync(FULL, T_lo < d)) + __popc(__ballot_sync(FULL, T_hi < d));
+    };
     // Copy of Q's unit of 16 pairs that starts the contraction for split pair
     // ps, its pairs below ps zeroed.  The split pair only moves forward and
     // mostly stays put, so an unchanged copy is kept.
@@ -602,18 +607,13 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       const int plo = plan >> 16, ps = plan & 0xFF;
       if (SPECIAL && (plan & kCorr)) {
         const int sk = j % NSK;
-        const uint32_t kb = sbase + L::OFF_K + sk * TILE;
         const bool need_sub = __any_sync(FULL, d_row > sT[min(ps, P - 1)]);
         const int T_add = ps > plo ? sT[ps - 1] : -1;
         const bool need_add = ps > plo && __any_sync(FULL, d_row >= 0 && d_row - (KT - 1) <= T_add);
-        // A pair's (g = 8: a group's) products for this warp's 32 rows by warp-level
-        // MMAs, m16n8k16: A = Q rows, dims 8 grp .. then P + 8 grp .. (a lane's
-        // register halves are pairs 8 grp + 2 (lane & 3) (+ 1), all but the pair's
-        // own zeroed), B = K rows.  S comes from TMEM in the layout of their
-        // accumulators (16 lanes x 256 bits), is their addend, and every element
-        // chooses by its distance.  (Through a scratch and row by row a pair took
+        // A pair's (g = 8: a group's) products are added to S, which comes from TMEM in
+        // the layout of MMA accumulators (16 lanes x 256 bits), every element
+        // choosing by its distance.  (Through a scratch and row by row a pair took
         // 450 cycles for 32 keys.)
-        const int qm = lane >> 3, qi = lane & 7;
         int pr[4];                             // distances of this lane's rows 8 k + lane / 4 to the tile's first key
 #pragma unroll
         for (int k = 0; k < 4; ++k) pr[k] = __shfl_sync(FULL, d_row, (lane >> 2) + 8 * k) - 2 * (lane & 3);
@@ -628,23 +628,22 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           const int dmax = d_last[1] - 32 * cc, dmin = max(d_first[0] - 32 * cc - 31, 0);
           if (dmax < 0) continue;              // wholly acausal
           // pairs ps .. pb - 1 are pruned somewhere in the chunk, pa .. ps - 1 kept somewhere
-          int pb = ps, pa = ps;
-          if (need_sub)
-            while (pb < P && sT[pb] < dmax) ++pb;
-          if (need_add && T_add >= dmin)
-            while (pa > plo && sT[pa - 1] >= dmin) --pa;
+          const int pb = need_sub ? max(ps, pairs_below(dmax)) : ps;
+          const int pa = need_add ? min(ps, max(plo, pairs_below(dmin))) : ps;
           if (pa >= pb) continue;
           uint32_t v[2][16];
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) tmem_ld_frag(tS + 32 * cc + (static_cast<uint32_t>(16 * mt) << 16), v[mt]);
           tmem_ld_wait();
-          uint32_t af[2][4], bf[4][2];
-          int cur = -1;
+          if constexpr (G8) {
+            // the group's products by warp-level MMAs, m16n8k16: A = Q rows, dims 8 grp
+            // .. then P + 8 grp .., B = K rows, S their addend
+            const uint32_t kb = sbase + L::OFF_K + sk * TILE;
+            const int qm = lane >> 3, qi = lane & 7;
+            uint32_t af[2][4], bf[4][2];
 #pragma unroll 1
-          for (int pp = pa; pp < pb; pp += G8 ? 8 : 1) {
-            const int grp = pp >> 3;
-            if (grp != cur) {
-              cur = grp;
+            for (int pp = pa; pp < pb; pp += 8) {
+              const int grp = pp >> 3;
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt)   // matrix m: rows 8 (m & 1) .., half m >> 1
                 ldsm_x4(smem_u32(smem_q) + ((qm >> 1) ? P / 8 + grp : grp) * COL + (wq * 32 + 16 * mt + 8 * (qm & 1) + qi) * 16,
@@ -656,33 +655,73 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                 ldsm_x4(kb + (key >> 3) * L::GROUP + (ch >> 3) * 1024 + (key & 7) * 128 + (((ch & 7) ^ (key & 7)) << 4),
                         bf[2 * hp][0], bf[2 * hp][1], bf[2 * hp + 1][0], bf[2 * hp + 1][1]);
               }
+              const bool sub = pp >= ps;
+              const uint32_t flip = sub ? 0x80008000u : 0u;   // subtract: Q with its sign turned
+              const int edge = 32 * cc + sT[pp];
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                // columns below d - edge are beyond the threshold: in none of the rows, or in all
+                if (sub ? d_last[mt] <= edge : d_first[mt] - edge >= 32) continue;
+                const int r0 = pr[2 * mt] - edge, r1 = pr[2 * mt + 1] - edge;
+                float z[4][4];
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) z[nt][e] = __uint_as_float(v[mt][4 * nt + e]);
+                  mma_16816_bf16(z[nt], af[mt][0] ^ flip, af[mt][1] ^ flip, af[mt][2] ^ flip, af[mt][3] ^ flip,
+                                 bf[nt][0], bf[nt][1]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const bool beyond = 8 * nt + (e & 1) < (e < 2 ? r0 : r1);
+                    v[mt][4 * nt + e] = beyond == sub ? __float_as_uint(z[nt][e]) : v[mt][4 * nt + e];
+                  }
+              }
             }
-            const bool sub = pp >= ps;
-            const uint32_t keep = G8 || (lane & 3) == ((pp & 7) >> 1) ? (G8 ? 0xFFFFFFFFu : (pp & 1) ? 0xFFFF0000u : 0x0000FFFFu)
-                                                                     : 0u;
-            const uint32_t flip = sub ? 0x80008000u & keep : 0u;   // subtract: Q with its sign turned
-            const int edge = 32 * cc + sT[pp];
+          } else {
+            // One pair is two products an element, on the FMA pipe: as an MMA with all
+            // but the pair's own dims zeroed it took twice as long.
+            const int c0 = 2 * (lane & 3);     // this lane's columns: c0 and c0 + 1 of each 8
+#pragma unroll 1
+            for (int pp = pa; pp < pb; ++pp) {
+              const bool sub = pp >= ps;
+              const int edge = 32 * cc + sT[pp];
+              const uint8_t* qa = smem_q + (pp >> 3) * COL + (wq * 32 + (lane >> 2)) * 16 + (pp & 7) * 2;
+              float q[4][2], k[4][2][2];       // [row 8 i][half]; [8 columns][column][half]
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              const uint32_t a0 = (af[mt][0] & keep) ^ flip, a1 = (af[mt][1] & keep) ^ flip;
-              const uint32_t a2 = (af[mt][2] & keep) ^ flip, a3 = (af[mt][3] & keep) ^ flip;
-              // columns below d - edge are beyond the threshold: in none of the rows, or in all
-              if (sub ? d_last[mt] <= edge : d_first[mt] - edge >= 32) continue;
-              const int r0 = pr[2 * mt] - edge, r1 = pr[2 * mt + 1] - edge;
-              float z[4][4];
+              for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int nt = 0; nt < 4; ++nt) {
+                for (int h = 0; h < 2; ++h) {
+                  const float x = bf16lo_to_f32(*reinterpret_cast<const uint16_t*>(qa + i * 128 + h * (P / 8) * COL));
+                  q[i][h] = sub ? -x : x;
+                }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[nt][e] = __uint_as_float(v[mt][4 * nt + e]);
-                mma_16816_bf16(z[nt], a0, a1, a2, a3, bf[nt][0], bf[nt][1]);
+              for (int h = 0; h < 2; ++h) {
+                const int ch = (pp >> 3) + h * (P / 8);
+                const uint8_t* ka = smem + L::OFF_K + sk * TILE + 4 * cc * L::GROUP + (ch >> 3) * 1024 + (pp & 7) * 2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                  for (int nt = 0; nt < 4; ++nt)
+                    k[nt][e][h] = bf16lo_to_f32(*reinterpret_cast<const uint16_t*>(
+                        ka + nt * L::GROUP + (c0 + e) * 128 + (((ch & 7) ^ (c0 + e)) << 4)));
               }
 #pragma unroll
-              for (int nt = 0; nt < 4; ++nt)
+              for (int i = 0; i < 4; ++i) {
+                const int rr = pr[i] - edge;   // columns below it are beyond the pair's threshold
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const bool beyond = 8 * nt + (e & 1) < (e < 2 ? r0 : r1);
-                  v[mt][4 * nt + e] = beyond == sub ? __float_as_uint(z[nt][e]) : v[mt][4 * nt + e];
+                for (int nt = 0; nt < 4; ++nt) {
+                  uint32_t& v0 = v[i >> 1][4 * nt + 2 * (i & 1)];
+                  uint32_t& v1 = v[i >> 1][4 * nt + 2 * (i & 1) + 1];
+                  float z0, z1;
+                  fma2(z0, z1, q[i][0], q[i][0], k[nt][0][0], k[nt][1][0], __uint_as_float(v0), __uint_as_float(v1));
+                  fma2(z0, z1, q[i][1], q[i][1], k[nt][0][1], k[nt][1][1], z0, z1);
+                  v0 = (8 * nt < rr) == sub ? __float_as_uint(z0) : v0;
+                  v1 = (8 * nt + 1 < rr) == sub ? __float_as_uint(z1) : v1;
                 }
+              }
             }
           }
 #pragma unroll
