@@ -116,24 +116,22 @@ def lib() -> ctypes.CDLL:
         L.wpattn_merge_lse.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp]
         L.wpattn_decode_paged.argtypes = [wp, vp, vp, vp, i32, i32, vp, i32, i32p, i32p, vp, i64,
                                           i32, i32, i32, f32, vp, vp, vp, ctypes.c_size_t, vp]
-        u8p, vpp, f64, sz = (ctypes.POINTER(ctypes.c_uint8), ctypes.POINTER(vp), ctypes.c_double,
-                             ctypes.c_size_t)
-        L.wpattn_prefill_paged.argtypes = [wp, vp, vp, vp, i32, i32, vp, i32, i32p, i32p, i32, i32, i32,
-                                           f32, vp, vp, vp, sz, vp]
+        f64, sz = ctypes.c_double, ctypes.c_size_t      # host arrays as plain pointers
+        L.wpattn_prefill_paged.argtypes = [wp, vp, vp, vp, i32, i32, vp, i32, vp, vp, i32, i32, i32, f32,
+                                           vp, vp, vp, sz, vp]
         L.wpattn_prefill_paged_workspace_size.restype = sz
-        L.wpattn_prefill_paged_workspace_size.argtypes = [wp, i32p, i32p, i32, i32, i32]
-        L.wpattn_rope_axes.argtypes = [vp, i64, vp, vp, i64, vp, i32, i32, i32, i32, vp, i64, i32, u8p,
-                                       f64, i32, vp]
-        L.wpattn_append_paged.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, vp, i32, i32p,
-                                          i32p, i32, i32, i32, i32, vp, i64, i32, u8p, f64, vp]
-        L.wpattn_pages_copy.argtypes = [vpp, i32, i32, i64, vp, vp, i32, vp]
+        L.wpattn_prefill_paged_workspace_size.argtypes = [wp, vp, vp, i32, i32, i32]
+        L.wpattn_rope_axes.argtypes = [vp, i64, vp, vp, i64, vp, i32, i32, i32, i32, vp, i64, i32, vp, f64,
+                                       i32, vp]
+        L.wpattn_append_paged.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, vp, i32, vp, vp,
+                                          i32, i32, i32, i32, vp, i64, i32, vp, f64, vp]
+        L.wpattn_pages_copy.argtypes = [vp, i32, i32, i64, vp, vp, i32, vp]
         L.wpattn_pages_workspace_size.restype = sz
         L.wpattn_pages_workspace_size.argtypes = [i32]
-        L.wpattn_pages_fork.argtypes = [vpp, i32, i32, i32, i64, vp, i32, i32, vp, i32p, i32p, i32p, i32,
-                                        vp, sz, vp]
-        L.wpattn_pages_free.argtypes = [i32, i32, vp, i32, i32, vp, i32p, i32p, i32, vp]
-        L.wpattn_pages_extend.argtypes = [i32, i32, vp, i32, i32, vp, i32p, i32p, i32p, i32, vp]
-        L.wpattn_pages_compact.argtypes = [vpp, i32, i32, i64, vp, i64, vp, vp, vp, sz, vp]
+        L.wpattn_pages_fork.argtypes = [vp, i32, i32, i32, i64, vp, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.wpattn_pages_free.argtypes = [i32, i32, vp, i32, i32, vp, vp, vp, i32, vp]
+        L.wpattn_pages_extend.argtypes = [i32, i32, vp, i32, i32, vp, vp, vp, vp, i32, vp]
+        L.wpattn_pages_compact.argtypes = [vp, i32, i32, i64, vp, i64, vp, vp, vp, sz, vp]
         L.wpattn_device_status.argtypes = [vp]
         L.wpattn_selftest_wait_timeout.argtypes = [vp]
         L.wpattn_strerror.restype = ctypes.c_char_p

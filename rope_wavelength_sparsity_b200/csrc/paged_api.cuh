@@ -19,10 +19,16 @@ bool page_size_ok(int page_size) {
 
 template <int MAXB>
 int launch_rope_axes(AxesParams<MAXB>& p, int D, int num_sms, cudaStream_t st) {
-  uint64_t per = 0;
-  for (int s = 0; s < p.nseg; ++s) per += (p.seg[s].H + 3) / 4;
-  const uint64_t items = static_cast<uint64_t>(p.tokens) * (D / 16) * per;
-  if (items == 0) return WPATTN_OK;
+  int batches = 0;
+  for (int s = 0; s < p.nseg; ++s) {
+    batches += (p.seg[s].H + 3) / 4;
+    p.turn |= p.seg[s].rotate;
+  }
+  // about a quarter of the GPU's threads at least
+  const uint64_t one = static_cast<uint64_t>(p.tokens) * (D / 16), enough = static_cast<uint64_t>(num_sms) * 512;
+  if (one == 0) return WPATTN_OK;
+  p.ways = static_cast<int>(std::min<uint64_t>(batches, (enough + one - 1) / one));
+  const uint64_t items = one * p.ways;
   const unsigned grid = static_cast<unsigned>(std::min<uint64_t>((items + 255) / 256, static_cast<uint64_t>(num_sms) * 8));
   if (D == 64) rope_axes_kernel<64, MAXB><<<grid, 256, 0, st>>>(p);
   else rope_axes_kernel<128, MAXB><<<grid, 256, 0, st>>>(p);
@@ -454,7 +460,7 @@ int wpattn_pages_copy(void* const* pools_host, int32_t n_pools, int32_t num_page
 }
 
 size_t wpattn_pages_workspace_size(int32_t num_pages) {
-  return num_pages > 0 ? (static_cast<size_t>(num_pages) * 2 + 2) * 4 + 4 * kPageRows : 0;
+  return num_pages > 0 ? (static_cast<size_t>(num_pages) * 3 + 2) * 4 + 4 * kPageRows : 0;
 }
 
 int wpattn_pages_fork(void* const* pools_host, int32_t n_pools, int32_t num_pages, int32_t page_size,

@@ -28,6 +28,8 @@ struct AxesParams {
   AxesSegment seg[3];
   int nseg;
   int tokens;
+  int ways;                // threads that share a token's batches of heads
+  int turn;                // some segment is rotated
   const int32_t* pos;      // [axes, pos_stride], or null: the token's row in its sequence
   int64_t pos_stride;
   int axes;
@@ -41,51 +43,51 @@ struct AxesParams {
   int kv_len[MAXB];        // its rows once the tokens are in
 };
 
-// One thread per (token, 8 pairs, segment, HB heads): the eight angles are
-// turned into cosines and sines once per thread; both 16-byte halves of up to
-// HB heads are loaded ahead of them.
+// One thread per (token, 8 pairs, way): of the segments' heads, taken HB at a time
+// one after another, a thread turns every ways-th batch.  It computes its eight
+// angles' cosines and sines once, under its first batch's loads, so one way is
+// best once the tokens alone fill the GPU (65000 tokens of 14 + 2 heads of 64:
+// 45 us with 1 way, 65 us with a thread per batch), and a way per batch when they
+// are few (64 tokens: one round trip instead of nine).
 template <int D, int MAXB>
 __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ AxesParams<MAXB> p) {
   constexpr int P = D / 2, NC = P / 8, HB = 4;
-  int groups[3], per = 0;                 // head groups of each segment
-  for (int s = 0; s < 3; ++s) {
-    groups[s] = s < p.nseg ? (p.seg[s].H + HB - 1) / HB : 0;
-    per += groups[s];
-  }
-  const uint64_t items = static_cast<uint64_t>(p.tokens) * NC * per;
+  const int b0 = (p.seg[0].H + HB - 1) / HB;                                   // batches up to each segment's end
+  const int b1 = b0 + (p.nseg > 1 ? (p.seg[1].H + HB - 1) / HB : 0);
+  const int b2 = b1 + (p.nseg > 2 ? (p.seg[2].H + HB - 1) / HB : 0);
+  const uint64_t items = static_cast<uint64_t>(p.tokens) * NC * p.ways;
   for (uint64_t idx = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x; idx < items;
        idx += static_cast<uint64_t>(gridDim.x) * blockDim.x) {
     const int c = static_cast<int>(idx % NC);
-    int hg = static_cast<int>(idx / NC % per), sg = 0;
-    const int token = static_cast<int>(idx / (static_cast<uint64_t>(NC) * per));
-    while (hg >= groups[sg]) hg -= groups[sg++];
-    const AxesSegment& g = p.seg[sg];
-    const int h0 = hg * HB, nb = min(HB, g.H - h0);
-    const uint16_t* src = g.src + token * g.src_stride + static_cast<int64_t>(h0) * D;
+    const int way = static_cast<int>(idx / NC % p.ways);
+    const int token = static_cast<int>(idx / NC / p.ways);
     uint4 lo[HB], hi[HB];
+    int sg = 0, h0 = 0, nb = 0;            // batch in registers
+    auto load = [&](int batch) {
+      sg = batch < b0 ? 0 : batch < b1 ? 1 : 2;
+      const AxesSegment& g = p.seg[sg];
+      h0 = (batch - (sg == 0 ? 0 : sg == 1 ? b0 : b1)) * HB;
+      nb = min(HB, g.H - h0);
+      const uint16_t* src = g.src + token * g.src_stride + static_cast<int64_t>(h0) * D;
 #pragma unroll
-    for (int u = 0; u < HB; ++u)
-      if (u < nb) {
-        lo[u] = *reinterpret_cast<const uint4*>(src + u * D + 8 * c);
-        hi[u] = *reinterpret_cast<const uint4*>(src + u * D + P + 8 * c);
-      }
-    int row = token;                      // the token's row in its sequence, and its pool row
-    int64_t to = token;
+      for (int u = 0; u < HB; ++u)
+        if (u < nb) {
+          lo[u] = *reinterpret_cast<const uint4*>(src + u * D + 8 * c);
+          hi[u] = *reinterpret_cast<const uint4*>(src + u * D + P + 8 * c);
+        }
+    };
+    load(way);
+    int row = token;                       // the token's row in its sequence, and its pool row (-1: none)
+    int64_t pool_row = token;
     if (p.block_table) {
       const int b = find_sequence(p.start, p.B, token);
       row = p.kv_len[b] - p.start[b + 1] + token;
-      if (g.paged) {
-        const int pg = p.block_table[static_cast<int64_t>(b) * p.max_pages + row / p.page_size];
-        if (pg < 0 || pg >= p.num_pages) {
-          record_status(6 /* WPATTN_EINDEX */);
-          continue;                       // nowhere to write
-        }
-        to = static_cast<int64_t>(pg) * p.page_size + row % p.page_size;
-      }
+      const int pg = p.block_table[static_cast<int64_t>(b) * p.max_pages + row / p.page_size];
+      if (pg < 0 || pg >= p.num_pages) record_status(6 /* WPATTN_EINDEX */);
+      pool_row = pg < 0 || pg >= p.num_pages ? -1 : static_cast<int64_t>(pg) * p.page_size + row % p.page_size;
     }
-    uint16_t* dst = g.dst + (to * g.H + h0) * D;
     float cs[8], sn[8];
-    if (g.rotate) {
+    if (p.turn) {
       int at[kMaxAxes];
 #pragma unroll
       for (int a = 0; a < kMaxAxes; ++a) at[a] = !p.pos ? row : a < p.axes ? p.pos[a * p.pos_stride + token] : 0;
@@ -96,25 +98,32 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
         sn[e] *= p.sign;
       }
     }
+    for (int batch = way; batch < b2; batch += p.ways) {
+      if (batch != way) load(batch);
+      const AxesSegment& g = p.seg[sg];
+      const int64_t to = g.paged ? pool_row : token;
+      if (to < 0) continue;                // nowhere to write
+      uint16_t* dst = g.dst + (to * g.H + h0) * D;
 #pragma unroll
-    for (int u = 0; u < HB; ++u)
-      if (u < nb) {
-        if (g.rotate) {
-          uint32_t a[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w}, b[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+      for (int u = 0; u < HB; ++u)
+        if (u < nb) {
+          if (g.rotate) {
+            uint32_t a[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w}, b[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float y0, y1, z0, z1;
-            rope_pair_bf16(bf16lo_to_f32(a[k]), bf16lo_to_f32(b[k]), cs[2 * k], sn[2 * k], y0, z0);
-            rope_pair_bf16(bf16hi_to_f32(a[k]), bf16hi_to_f32(b[k]), cs[2 * k + 1], sn[2 * k + 1], y1, z1);
-            a[k] = pack_bf16x2(y0, y1);
-            b[k] = pack_bf16x2(z0, z1);
+            for (int k = 0; k < 4; ++k) {
+              float y0, y1, z0, z1;
+              rope_pair_bf16(bf16lo_to_f32(a[k]), bf16lo_to_f32(b[k]), cs[2 * k], sn[2 * k], y0, z0);
+              rope_pair_bf16(bf16hi_to_f32(a[k]), bf16hi_to_f32(b[k]), cs[2 * k + 1], sn[2 * k + 1], y1, z1);
+              a[k] = pack_bf16x2(y0, y1);
+              b[k] = pack_bf16x2(z0, z1);
+            }
+            lo[u] = make_uint4(a[0], a[1], a[2], a[3]);
+            hi[u] = make_uint4(b[0], b[1], b[2], b[3]);
           }
-          lo[u] = make_uint4(a[0], a[1], a[2], a[3]);
-          hi[u] = make_uint4(b[0], b[1], b[2], b[3]);
+          *reinterpret_cast<uint4*>(dst + u * D + 8 * c) = lo[u];
+          *reinterpret_cast<uint4*>(dst + u * D + P + 8 * c) = hi[u];
         }
-        *reinterpret_cast<uint4*>(dst + u * D + 8 * c) = lo[u];
-        *reinterpret_cast<uint4*>(dst + u * D + P + 8 * c) = hi[u];
-      }
+    }
   }
 }
 
@@ -157,6 +166,22 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   __syncthreads();                    // warp_sums may be reused
   return before + x - v;
 }
+
+// This block's share of a copy of 16-byte units: four loads ahead of their stores.
+__device__ __forceinline__ void block_copy(uint8_t* __restrict__ dst, const uint8_t* __restrict__ src, int64_t units) {
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  for (int64_t i = threadIdx.x; i < units; i += 4 * blockDim.x) {
+    uint4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * blockDim.x < units) x[k] = s[i + k * blockDim.x];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * blockDim.x < units) d[i + k * blockDim.x] = x[k];
+  }
+}
+constexpr int kCopyUnits = 1024;       // 16-byte units (16 KB) of one page that a block copies at a time
 
 // The lowest `want` free pages, in order, into list; -1 where there are fewer.
 __global__ void __launch_bounds__(kScanThreads)
@@ -213,14 +238,13 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkP
     if (threadIdx.x == 0) record_status(6 /* WPATTN_EINDEX */);
     return;
   }
-  const int64_t page_bytes = p.row_bytes * p.page_size, chunks = p.row_bytes * part / 16;
-  const int64_t all = chunks * p.pools.n;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    uint8_t* pool = p.pools.pool[i / chunks];
-    const int64_t at = i % chunks * 16;
-    *reinterpret_cast<uint4*>(pool + fresh * page_bytes + at) =
-        *reinterpret_cast<const uint4*>(pool + old * page_bytes + at);
+  const int64_t page_bytes = p.row_bytes * p.page_size, units = p.row_bytes * part / 16;
+  const int64_t pieces = (units + kCopyUnits - 1) / kCopyUnits;
+  for (int64_t i = blockIdx.x; i < pieces * p.pools.n; i += gridDim.x) {
+    uint8_t* pool = p.pools.pool[i / pieces];
+    const int64_t at = i % pieces * kCopyUnits;
+    block_copy(pool + fresh * page_bytes + at * 16, pool + old * page_bytes + at * 16,
+               min(static_cast<int64_t>(kCopyUnits), units - at));
   }
 }
 
@@ -280,27 +304,45 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const __grid_const
   for (int r = found + threadIdx.x; r < want; r += kScanThreads) put(r, -1);
 }
 
-// ws: [0] live pages, [1] moves, then per page: free slot of rank k at
-// ws[2 + k], and rank of a page that moves (or -1) at ws[2 + num_pages + page].
+// ws: [0] live pages, [1] moves; then, num_pages of each: the free slot of rank k,
+// the moving page of rank k, and each page's rank among those that move (or -1).
+// A thread takes four pages at a time and scans both counts at once (each at
+// most 4096 a round, in 16 bits).
 __global__ void __launch_bounds__(kScanThreads)
 compact_plan_kernel(const int32_t* __restrict__ refs, int num_pages, int32_t* __restrict__ ws,
                     int32_t* __restrict__ live_out) {
   __shared__ int sums[kScanThreads / 32];
+  int32_t* slot = ws + 2;
+  int32_t* from = slot + num_pages;
+  int32_t* rank = from + num_pages;
   int total, mine = 0;
+#pragma unroll 4
   for (int i = threadIdx.x; i < num_pages; i += kScanThreads) mine += refs[i] > 0 ? 1 : 0;
   block_scan(mine, sums, &total);
   const int live = total;
   int holes = 0, moves = 0;
-  for (int base = 0; base < num_pages; base += kScanThreads) {
-    const int i = base + threadIdx.x;
-    const bool used = i < num_pages && refs[i] > 0;
-    const int hole = i < live && !used ? 1 : 0, move = i >= live && used ? 1 : 0;
-    int th, tm;
-    const int ah = holes + block_scan(hole, sums, &th), am = moves + block_scan(move, sums, &tm);
-    if (hole) ws[2 + ah] = i;
-    if (i < num_pages) ws[2 + num_pages + i] = move ? am : -1;
-    holes += th;
-    moves += tm;
+  for (int base = 0; base < num_pages; base += 4 * kScanThreads) {
+    const int i0 = base + 4 * threadIdx.x;
+    bool hole[4], move[4];
+    int both = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool used = i0 + k < num_pages && refs[i0 + k] > 0;
+      hole[k] = i0 + k < live && !used;
+      move[k] = i0 + k >= live && used;
+      both += (hole[k] ? 1 : 0) | (move[k] ? 1 << 16 : 0);
+    }
+    const int at = block_scan(both, sums, &total);
+    int ah = holes + (at & 0xFFFF), am = moves + (at >> 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k < num_pages) {
+        if (hole[k]) slot[ah++] = i0 + k;
+        rank[i0 + k] = move[k] ? am : -1;
+        if (move[k]) from[am++] = i0 + k;
+      }
+    holes += total & 0xFFFF;
+    moves += total >> 16;
   }
   if (threadIdx.x == 0) {
     ws[0] = live;
@@ -319,27 +361,27 @@ struct CompactParams {
   int64_t page_bytes;
 };
 
-// Blocks take pages in turn and move those that the plan moves; then the
-// table's entries follow.
+// Blocks take pieces of the moving pages in turn; then the table's entries and the
+// refs follow.
 __global__ void __launch_bounds__(256) compact_kernel(const __grid_constant__ CompactParams p) {
   const int32_t* slot = p.ws + 2;
-  const int32_t* rank = p.ws + 2 + p.num_pages;
-  for (int i = blockIdx.x; i < p.num_pages; i += gridDim.x) {
-    if (rank[i] < 0) continue;
-    const int to = slot[rank[i]];
-    for (int n = 0; n < p.pools.n; ++n) {
-      const uint8_t* s = p.pools.pool[n] + i * p.page_bytes;
-      uint8_t* d = p.pools.pool[n] + to * p.page_bytes;
-      for (int64_t at = threadIdx.x * 16; at < p.page_bytes; at += blockDim.x * 16)
-        *reinterpret_cast<uint4*>(d + at) = *reinterpret_cast<const uint4*>(s + at);
-    }
-    if (threadIdx.x == 0) {
-      p.refs[to] = p.refs[i];
-      p.refs[i] = 0;
-    }
+  const int32_t* from = slot + p.num_pages;
+  const int32_t* rank = from + p.num_pages;
+  const int64_t moves = p.ws[1], units = p.page_bytes / 16, pieces = (units + kCopyUnits - 1) / kCopyUnits;
+  for (int64_t i = blockIdx.x; i < moves * p.pools.n * pieces; i += gridDim.x) {
+    const int64_t page = i / pieces % moves;
+    uint8_t* pool = p.pools.pool[i / pieces / moves];
+    const int64_t at = i % pieces * kCopyUnits;
+    block_copy(pool + slot[page] * p.page_bytes + at * 16, pool + from[page] * p.page_bytes + at * 16,
+               min(static_cast<int64_t>(kCopyUnits), units - at));
   }
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < p.entries;
-       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t k = first; k < moves; k += stride) {
+    p.refs[slot[k]] = p.refs[from[k]];
+    p.refs[from[k]] = 0;
+  }
+  for (int64_t e = first; e < p.entries; e += stride) {
     const int pg = p.table[e];
     if (pg >= 0 && pg < p.num_pages && rank[pg] >= 0) p.table[e] = slot[rank[pg]];
   }
@@ -362,9 +404,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
       if (threadIdx.x == 0) record_status(6 /* WPATTN_EINDEX */);
       continue;
     }
-    for (int64_t at = threadIdx.x * 16; at < p.page_bytes; at += blockDim.x * 16)
-      *reinterpret_cast<uint4*>(pool + d * p.page_bytes + at) =
-          *reinterpret_cast<const uint4*>(pool + s * p.page_bytes + at);
+    block_copy(pool + d * p.page_bytes, pool + s * p.page_bytes, p.page_bytes / 16);
   }
 }
 

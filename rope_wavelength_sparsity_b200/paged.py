@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+from array import array
 
 import torch
 
@@ -31,18 +32,24 @@ def _on(t, stream):
     return _NOTHING if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
-def _stream():
-    return torch.cuda.current_stream().cuda_stream
+def _stream(t):
+    """torch's current stream of t's device, as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _ints(values, n=None, what="lengths"):
-    values = [int(x) for x in values]
-    if n is not None and len(values) != n:
-        raise ValueError(f"{what} has {len(values)} entries, expected {n}")
-    for x in values:
-        if not -2**31 <= x < 2**31:
-            raise ValueError(f"{what}: {x} is not a 32-bit integer")
-    return (ctypes.c_int32 * len(values))(*values)
+    """Host ints as an array of int32; pass ``.buffer_info()[0]`` on."""
+    try:
+        a = array("i", values)
+    except OverflowError as e:
+        raise ValueError(f"{what}: {e}") from None
+    if n is not None and len(a) != n:
+        raise ValueError(f"{what} has {len(a)} entries, expected {n}")
+    return a
+
+
+def _at(a):
+    return a.buffer_info()[0]
 
 
 def _tensor(t, name, dtype, like=None, shape=None):
@@ -94,8 +101,8 @@ def _table(block_table, like, rows=None):
 def prefill_paged_workspace_size(w: Window, q_len, kv_len, Hq: int, Hkv: int) -> int:
     """Workspace bytes of ``prefill_paged`` on the current device."""
     B = len(q_len)
-    return int(lib().wpattn_prefill_paged_workspace_size(ctypes.byref(w._c()), _ints(q_len), _ints(kv_len, B), B,
-                                                         Hq, Hkv))
+    ql, kl = _ints(q_len), _ints(kv_len, B)
+    return int(lib().wpattn_prefill_paged_workspace_size(ctypes.byref(w._c()), _at(ql), _at(kl), B, Hq, Hkv))
 
 
 def prefill_paged(q, k_pages, v_pages, block_table, q_len, kv_len, w: Window, *, scale: float | None = None,
@@ -130,18 +137,18 @@ def prefill_paged(q, k_pages, v_pages, block_table, q_len, kv_len, w: Window, *,
     L, cw = lib(), ctypes.byref(w._c())
     with _on(q, stream):
         if workspace is None:
-            need = L.wpattn_prefill_paged_workspace_size(cw, ql, kl, B, Hq, Hkv)
+            need = L.wpattn_prefill_paged_workspace_size(cw, _at(ql), _at(kl), B, Hq, Hkv)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         if out is None:
             out = torch.empty_like(q)
         if lse is None and want_lse:
             lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-        rc = L.wpattn_prefill_paged(cw, qp, kp, vp, num_pages, page_size, tp, block_table.shape[1], ql, kl, B, Hq,
-                                    Hkv, float(scale) if scale else 0.0, out.data_ptr(),
+        rc = L.wpattn_prefill_paged(cw, qp, kp, vp, num_pages, page_size, tp, block_table.shape[1], _at(ql), _at(kl), B,
+                                    Hq, Hkv, float(scale) if scale else 0.0, out.data_ptr(),
                                     lse.data_ptr() if lse is not None else None,
                                     workspace.data_ptr() if workspace is not None else None,
-                                    workspace.numel() if workspace is not None else 0, _stream())
+                                    workspace.numel() if workspace is not None else 0, _stream(q))
     _check(rc, "wpattn_prefill_paged")
     return out, lse
 
@@ -159,10 +166,10 @@ def _positions(positions, tokens, like):
 def _pair_axes(pair_axes, D, axes):
     if pair_axes is None:
         return None
-    pair_axes = [int(a) for a in pair_axes]
-    if len(pair_axes) != D // 2 or not all(0 <= a < axes for a in pair_axes):
+    pair_axes = bytes(pair_axes)               # refuses what is not in 0 .. 255
+    if len(pair_axes) != D // 2 or max(pair_axes) >= axes:
         raise ValueError(f"pair_axes must name one of {axes} axes for each of {D // 2} pairs")
-    return (ctypes.c_uint8 * len(pair_axes))(*pair_axes)
+    return pair_axes
 
 
 def rope_axes(q, k, positions, pair_axes=None, *, base: float, inverse: bool = False, q_out=None, k_out=None,
@@ -193,7 +200,7 @@ def rope_axes(q, k, positions, pair_axes=None, *, base: float, inverse: bool = F
         if k is not None and k_out is None:
             k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device)
         rc = lib().wpattn_rope_axes(qp, qs, q_out.data_ptr(), kp, ks, k_out.data_ptr() if k is not None else None, T,
-                                    Hq, Hkv, D, pp, pstride, axes, pa, float(base), int(bool(inverse)), _stream())
+                                    Hq, Hkv, D, pp, pstride, axes, pa, float(base), int(bool(inverse)), _stream(q))
     _check(rc, "wpattn_rope_axes")
     return q_out, k_out
 
@@ -239,8 +246,8 @@ def append_paged(k, v, k_pages, v_pages, block_table, new_len, kv_len, *, q=None
         if q is not None and q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
         rc = lib().wpattn_append_paged(kp, ks, vp, vs, qp, qs, q_out.data_ptr() if q is not None else None, kpp, vpp,
-                                       num_pages, page_size, tp, block_table.shape[1], nl, kl, B, Hq, Hkv, D, pp,
-                                       pstride, axes, pa, 0.0 if base is None else float(base), _stream())
+                                       num_pages, page_size, tp, block_table.shape[1], _at(nl), _at(kl), B, Hq, Hkv, D, pp,
+                                       pstride, axes, pa, 0.0 if base is None else float(base), _stream(k))
     _check(rc, "wpattn_append_paged")
     return q_out
 
@@ -281,7 +288,7 @@ def pages_copy(pools, src, dst, *, stream=None):
     sp, dp = _tensor(src, "src", torch.int32), _tensor(dst, "dst", torch.int32, src, src.shape)
     array, n, page_bytes = _pools(pools, src, pages_known=False)
     with _on(src, stream):
-        rc = lib().wpattn_pages_copy(array, n, pools[0].shape[0], page_bytes, sp, dp, src.shape[0], _stream())
+        rc = lib().wpattn_pages_copy(array, n, pools[0].shape[0], page_bytes, sp, dp, src.shape[0], _stream(src))
     _check(rc, "wpattn_pages_copy")
 
 
@@ -300,8 +307,8 @@ def pages_fork(pools, block_table, refs, src_rows, dst_rows, lens, *, workspace=
     with _on(refs, stream):
         workspace = _pages_workspace(workspace, refs)
         rc = lib().wpattn_pages_fork(array, n_pools, refs.shape[0], page_size, page_bytes // page_size, tp,
-                                     block_table.shape[0], block_table.shape[1], rp, src, dst, ln, n,
-                                     workspace.data_ptr(), workspace.numel(), _stream())
+                                     block_table.shape[0], block_table.shape[1], rp, _at(src), _at(dst), _at(ln), n,
+                                     workspace.data_ptr(), workspace.numel(), _stream(refs))
     _check(rc, "wpattn_pages_fork")
 
 
@@ -311,8 +318,8 @@ def pages_free(block_table, refs, rows, lens, page_size: int, *, stream=None):
     r = _ints(rows, None, "rows")
     ln = _ints(lens, len(r), "lens")
     with _on(refs, stream):
-        rc = lib().wpattn_pages_free(refs.shape[0], page_size, tp, block_table.shape[0], block_table.shape[1], rp, r,
-                                     ln, len(r), _stream())
+        rc = lib().wpattn_pages_free(refs.shape[0], page_size, tp, block_table.shape[0], block_table.shape[1], rp, _at(r),
+                                     _at(ln), len(r), _stream(refs))
     _check(rc, "wpattn_pages_free")
 
 
@@ -322,8 +329,8 @@ def pages_extend(block_table, refs, rows, lens, new_lens, page_size: int, *, str
     r = _ints(rows, None, "rows")
     a, b = _ints(lens, len(r), "lens"), _ints(new_lens, len(r), "new_lens")
     with _on(refs, stream):
-        rc = lib().wpattn_pages_extend(refs.shape[0], page_size, tp, block_table.shape[0], block_table.shape[1], rp, r,
-                                       a, b, len(r), _stream())
+        rc = lib().wpattn_pages_extend(refs.shape[0], page_size, tp, block_table.shape[0], block_table.shape[1], rp, _at(r),
+                                       _at(a), _at(b), len(r), _stream(refs))
     _check(rc, "wpattn_pages_extend")
 
 
@@ -336,6 +343,6 @@ def pages_compact(pools, block_table, refs, *, workspace=None, stream=None):
         workspace = _pages_workspace(workspace, refs)
         live = torch.empty(1, dtype=torch.int32, device=refs.device)
         rc = lib().wpattn_pages_compact(array, n_pools, refs.shape[0], page_bytes, tp, block_table.numel(), rp,
-                                        live.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream())
+                                        live.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(refs))
     _check(rc, "wpattn_pages_compact")
     return live
