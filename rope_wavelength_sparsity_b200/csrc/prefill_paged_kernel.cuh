@@ -150,8 +150,8 @@ struct PagedSmem {
   static constexpr int OFF_T = OFF_QM + 2 * 4 * COL;
   static constexpr int OFF_PS = OFF_T + 64 * 4;      // plan of each tile's next step
   static constexpr int OFF_LEFT = OFF_PS + 4 * 4;    // warps of each softmax group that left a corrected K tile
-  static constexpr int OFF_BUSY = OFF_LEFT + 4 * 4;  // softmax warps at their exponentials
-  static constexpr int OFF_BAR = OFF_BUSY + 8 * 4;
+  static constexpr int OFF_TURN = OFF_LEFT + 4 * 4;  // per softmax warp: the step whose exponentials are its next
+  static constexpr int OFF_BAR = OFF_TURN + 8 * 4;
   // k_full, k_empty [NSK], v_full, v_empty [NSV], s_full, p_most, p_full, o_final, q_ready, s_left, pv_done [2], v_fix
   static constexpr int NBAR = 2 * NSK + 2 * NSV + 15;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
@@ -281,7 +281,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   const bool tail = steps > 0 && top == nkt - 1 && it.kv_len % KT != 0;
 
   if (threadIdx.x < 64) sT[threadIdx.x] = p.T[threadIdx.x];
-  if (threadIdx.x < 12) reinterpret_cast<int*>(smem + L::OFF_LEFT)[threadIdx.x] = 0;   // OFF_BUSY too
+  if (threadIdx.x < 4) reinterpret_cast<int*>(smem + L::OFF_LEFT)[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSK; ++s) {
       mbar_init(k_full(s), 1);
@@ -489,7 +489,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     uint8_t* smem_q = smem + ((dup || t == 0) ? L::OFF_Q0 : L::OFF_Q1);
     uint8_t* smem_qm = smem + L::OFF_QM + t * 4 * COL;
     const int my_last = t == 0 ? kt_last[0] : kt_last[1];
-    volatile int* busy = reinterpret_cast<volatile int*>(smem + L::OFF_BUSY);
+    volatile int* turn = reinterpret_cast<volatile int*>(smem + L::OFF_TURN);
     float m_ref = -INFINITY;   // exponent reference of O and l (log2 units)
     float l_run = 0.f;
     int cnt = 0;
@@ -502,6 +502,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         *reinterpret_cast<uint4*>(smem_q + c * COL + r * 16) = row_ok ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
     }
+    const int stride = dup ? 2 : 1;            // this tile's steps: every stride-th from j0 on
+    const int j0 = dup ? t : top - my_last;
+    if (lane == 0) turn[warp] = j0;
     asm volatile("bar.sync 1, 256;" ::: "memory");   // dup: group 1 reads group 0's rows
 
     // The first pair kept somewhere in step j (plo) and the split pair (ps) of a pair
@@ -521,8 +524,6 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     // .. P - 1 are contracted and subtracted where they are pruned.  At the
     // pair first kept 32 past the tile's centre distance both sets are small
     // (thresholds grow geometrically).  Any ps >= plo gives the same scores.
-    const int stride = dup ? 2 : 1;            // this tile's steps: every stride-th from j0 on
-    const int j0 = dup ? t : top - my_last;
     Cursor low{0, sT[0]}, far = low;
     int ps_now = P, T_ps = 0, T_before = 0;    // of the latest plan; thresholds of ps and the pair before
     int quiet = 0;                             // steps behind the latest planned one that have the same plan
@@ -796,19 +797,13 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       // p, rounded to bf16 (the MMA's operand type); l sums them unrounded
       {
         float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
-        // Warps w and w + 4 share an SM partition and its exponentials: they take turns
-        // (tile 0 first when both come at once), so that one's products run under
-        // the other's exponentials.  Side by side both would wait for both.  The
-        // wait is short and may be given up: it orders nothing.
+        // Warps w and w + 4 share an SM partition and its exponentials.  They take
+        // turns, tile 0 first in each step, so that one tile's other work runs
+        // under the other's exponentials (side by side both would wait for both),
+        // in the same order on every partition (or a tile waits for its last
+        // warp).  The wait is bounded and may be given up: it orders nothing.
 #pragma unroll 1
-        for (int i = 0; i < 64 && busy[warp ^ 4]; ++i) {}
-        if (lane == 0) busy[warp] = 1;
-        if (t == 1 && busy[warp ^ 4]) {
-          if (lane == 0) busy[warp] = 0;
-#pragma unroll 1
-          for (int i = 0; i < 64 && busy[warp ^ 4]; ++i) {}
-          if (lane == 0) busy[warp] = 1;
-        }
+        for (int i = 0; i < 256 && turn[warp ^ 4] < (t && !dup ? j + 1 : j); ++i) {}
         asm volatile("" : "+f"(nm));           // no exponential above this
         float acc[8];
 #pragma unroll
@@ -832,7 +827,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           }
         }
         tmem_st16u(tP + 48, pk2 + 48);
-        if (lane == 0) busy[warp] = 0;
+        if (lane == 0) turn[warp] = j + 1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -852,6 +847,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       ++cnt;
       plan = plan_next;
     }
+    if (lane == 0) turn[warp] = 0x7FFFFFFF;
 
     // ----------------------------------------------------------- epilogue
     (void)__all_sync(FULL, mbar_wait(o_final(t), 0));     // this tile's products have completed
