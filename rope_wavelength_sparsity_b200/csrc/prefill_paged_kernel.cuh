@@ -160,6 +160,17 @@ struct PagedSmem {
 static_assert(PagedSmem<64>::NSK % 2 == 0 && PagedSmem<128>::NSK % 2 == 0, "even rings");
 static_assert(PagedSmem<128>::ALLOC <= 232448 && PagedSmem<64>::ALLOC <= 232448, "shared memory of one CTA");
 
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16u(uint32_t taddr, uint32_t* u) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr));
+}
+
 // 32 columns of 16 TMEM lanes in the layout of four m16n8 MMA accumulators: register
 // 4 i + e is row lane / 4 + 8 (e >> 1), column 8 i + 2 (lane % 4) + (e & 1).
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&u)[16]) {
