@@ -114,6 +114,47 @@ int64_t sum_lengths(const int32_t* len, int32_t B) {
   return sum <= INT32_MAX ? sum : -1;
 }
 
+template <int MAXN>
+int launch_fork(const PagePools& pools, int num_pages, int page_size, int64_t row_bytes, int32_t* table,
+                int max_pages, int32_t* refs, const int32_t* src, const int32_t* dst, const int32_t* len, int n,
+                int32_t* list, int num_sms, cudaStream_t st) {
+  ForkParams<MAXN> p;
+  p.pools = pools;
+  int begun = 0, most = 0;
+  for (int i = 0; i < n; ++i) {
+    p.src[i] = src[i];
+    p.dst[i] = dst[i];
+    p.len[i] = len[i];
+    p.rank[i] = len[i] % page_size ? begun++ : -1;
+    most = std::max(most, len[i] % page_size);
+  }
+  if (begun > 0) {
+    find_free_pages_kernel<<<1, kScanThreads, 0, st>>>(refs, num_pages, list, begun);
+    const int rc = launched();
+    if (rc != WPATTN_OK) return rc;
+  }
+  p.table = table; p.refs = refs; p.list = list;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size; p.n = n;
+  p.row_bytes = row_bytes;
+  // 16 KB of copies a block, at most about eight blocks an SM
+  const int64_t per_fork = row_bytes * most * pools.n;
+  const int64_t x = std::max<int64_t>(1, std::min<int64_t>((per_fork + 16383) / 16384, int64_t(num_sms) * 8 / n + 1));
+  fork_kernel<MAXN><<<dim3(static_cast<unsigned>(x), n), 256, 0, st>>>(p);
+  return launched();
+}
+
+template <int MAXN>
+int launch_free(int num_pages, int page_size, int32_t* table, int max_pages, int32_t* refs, const int32_t* rows,
+                const int32_t* len, int n, int most_pages, cudaStream_t st) {
+  RowsParams<MAXN> p;
+  std::copy(rows, rows + n, p.row);
+  std::copy(len, len + n, p.len);
+  p.table = table; p.refs = refs;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size; p.n = n;
+  free_kernel<MAXN><<<dim3((most_pages + 255) / 256, n), 256, 0, st>>>(p);
+  return launched();
+}
+
 // ------------------------------------------------------------ prefill_paged: plan and launch
 // Which CTAs run a call: sequences in order, each with the parts its row
 // blocks' key ranges are cut into; those with several parts come first.
@@ -469,9 +510,8 @@ int wpattn_pages_fork(void* const* pools_host, int32_t n_pools, int32_t num_page
                       const int32_t* len_host, int32_t n, void* workspace, size_t workspace_bytes,
                       void* cuda_stream) {
   if (page_size <= 0 || row_bytes <= 0 || row_bytes % 16) return WPATTN_EINVAL;
-  ForkParams p;
-  std::memset(&p, 0, sizeof p);
-  int rc = set_pools(&p.pools, pools_host, n_pools, row_bytes * page_size);
+  PagePools pools;
+  int rc = set_pools(&pools, pools_host, n_pools, row_bytes * page_size);
   if (rc != WPATTN_OK) return rc;
   if (n < 0 || num_pages <= 0 || num_rows <= 0 || max_pages <= 0) return WPATTN_EINVAL;
   if (n > kPageRows) return WPATTN_EUNSUPPORTED;
@@ -481,36 +521,17 @@ int wpattn_pages_fork(void* const* pools_host, int32_t n_pools, int32_t num_page
     return WPATTN_EINVAL;
   int32_t dsts[kPageRows];
   if (!rows_ok(dst_rows_host, n, num_rows, dsts)) return WPATTN_EINVAL;
-  int begun = 0, most = 0;
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < n; ++i)
     if (src_rows_host[i] < 0 || src_rows_host[i] >= num_rows || len_host[i] < 0 ||
-        len_host[i] > int64_t(max_pages) * page_size ||
-        std::binary_search(dsts, dsts + n, src_rows_host[i]))
+        len_host[i] > int64_t(max_pages) * page_size || std::binary_search(dsts, dsts + n, src_rows_host[i]))
       return WPATTN_EINVAL;
-    p.src[i] = src_rows_host[i];
-    p.dst[i] = dst_rows_host[i];
-    p.len[i] = len_host[i];
-    p.rank[i] = len_host[i] % page_size ? begun++ : -1;
-    most = std::max(most, len_host[i] % page_size);
-  }
   if (!workspace || workspace_bytes < wpattn_pages_workspace_size(num_pages)) return WPATTN_EWORKSPACE;
   if (!aligned16(workspace)) return WPATTN_EINVAL;
   DeviceInfo* dev = nullptr;
   if ((rc = device_info(&dev)) != WPATTN_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  int32_t* list = static_cast<int32_t*>(workspace);
-  if (begun > 0) {
-    find_free_pages_kernel<<<1, kScanThreads, 0, st>>>(refs, num_pages, list, begun);
-    if ((rc = launched()) != WPATTN_OK) return rc;
-  }
-  p.table = block_table; p.refs = refs; p.list = list;
-  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size; p.n = n;
-  p.row_bytes = row_bytes;
-  // 16 KB of copies a block, at most about eight blocks an SM
-  const int64_t per_fork = row_bytes * most * n_pools;
-  const int64_t x = std::max<int64_t>(1, std::min<int64_t>((per_fork + 16383) / 16384, int64_t(dev->num_sms) * 8 / n + 1));
-  fork_kernel<<<dim3(static_cast<unsigned>(x), n), 256, 0, st>>>(p);
-  return launched();
+  const auto fork = n <= kFewRows ? launch_fork<kFewRows> : launch_fork<kPageRows>;
+  return fork(pools, num_pages, page_size, row_bytes, block_table, max_pages, refs, src_rows_host, dst_rows_host,
+              len_host, n, static_cast<int32_t*>(workspace), dev->num_sms, static_cast<cudaStream_t>(cuda_stream));
 }
 
 int wpattn_pages_free(int32_t num_pages, int32_t page_size, int32_t* block_table, int32_t num_rows,
@@ -523,24 +544,18 @@ int wpattn_pages_free(int32_t num_pages, int32_t page_size, int32_t* block_table
   if (!block_table || !refs || !rows_host || !len_host || !aligned4(block_table) || !aligned4(refs) ||
       !rows_ok(rows_host, n, num_rows, sorted))
     return WPATTN_EINVAL;
-  RowsParams p;
-  std::memset(&p, 0, sizeof p);
   int longest = 0;
   for (int i = 0; i < n; ++i) {
     if (len_host[i] < 0 || len_host[i] > int64_t(max_pages) * page_size) return WPATTN_EINVAL;
-    p.row[i] = rows_host[i];
-    p.len[i] = len_host[i];
     longest = std::max(longest, len_host[i]);
   }
   if (longest == 0) return WPATTN_OK;
   DeviceInfo* dev = nullptr;
   const int rc = device_info(&dev);
   if (rc != WPATTN_OK) return rc;
-  p.table = block_table; p.refs = refs;
-  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size; p.n = n;
-  const int pages = (longest + page_size - 1) / page_size;
-  free_kernel<<<dim3((pages + 255) / 256, n), 256, 0, static_cast<cudaStream_t>(cuda_stream)>>>(p);
-  return launched();
+  const auto give_back = n <= kFewRows ? launch_free<kFewRows> : launch_free<kPageRows>;
+  return give_back(num_pages, page_size, block_table, max_pages, refs, rows_host, len_host, n,
+                   (longest + page_size - 1) / page_size, static_cast<cudaStream_t>(cuda_stream));
 }
 
 int wpattn_pages_extend(int32_t num_pages, int32_t page_size, int32_t* block_table, int32_t num_rows,

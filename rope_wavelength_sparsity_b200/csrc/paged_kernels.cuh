@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
 // not depend on how its threads are scheduled.
 constexpr int kMaxPools = 256;
 constexpr int kPageRows = 1024;     // table rows one call may name
+constexpr int kFewRows = 64;        // up to so many take launches with shorter parameters
 constexpr int kScanThreads = 1024;
 
 struct PagePools {
@@ -199,6 +200,7 @@ find_free_pages_kernel(const int32_t* __restrict__ refs, int num_pages, int32_t*
   for (int i = found + threadIdx.x; i < want; i += kScanThreads) list[i] = -1;
 }
 
+template <int MAXN>
 struct ForkParams {
   PagePools pools;
   int32_t* table;          // [rows, max_pages]
@@ -206,12 +208,13 @@ struct ForkParams {
   const int32_t* list;     // a free page for each fork with a begun page, in order
   int num_pages, max_pages, page_size, n;
   int64_t row_bytes;       // bytes of one key's heads in a pool
-  int src[kPageRows], dst[kPageRows], len[kPageRows];
-  int rank[kPageRows];     // index into list, -1: the last page is full
+  int src[MAXN], dst[MAXN], len[MAXN];
+  int rank[MAXN];          // index into list, -1: the last page is full
 };
 
 // Block (x, f): fork f.  Its table row first (x = 0), then its begun page.
-__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkParams p) {
+template <int MAXN>
+__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkParams<MAXN> p) {
   const int f = blockIdx.y;
   const int full = p.len[f] / p.page_size, part = p.len[f] % p.page_size;
   const int32_t* from = p.table + static_cast<int64_t>(p.src[f]) * p.max_pages;
@@ -248,15 +251,17 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkP
   }
 }
 
+template <int MAXN>
 struct RowsParams {
   int32_t* table;
   int32_t* refs;
   int num_pages, max_pages, page_size, n;
-  int row[kPageRows], len[kPageRows];
+  int row[MAXN], len[MAXN];
 };
 
 // Block (x, i): row i gives back its pages and its entries become -1.
-__global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ RowsParams p) {
+template <int MAXN>
+__global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ RowsParams<MAXN> p) {
   const int i = blockIdx.y;
   const int pages = (p.len[i] + p.page_size - 1) / p.page_size;
   int32_t* row = p.table + static_cast<int64_t>(p.row[i]) * p.max_pages;
