@@ -518,8 +518,8 @@ WPATTN_API int wpattn_merge_lse(const void *outs, const float *lses, int32_t R, 
  *                WPATTN_EWORKSPACE); may be NULL when that is 0.  Two calls
  *                that can overlap on the GPU need one each.
  * Rows of the pools behind a sequence's last key hold anything (NaN
- * included); a non-finite V among a sequence's keys may reach queries of the
- * chunk before it.  Requires D in {64, 128}, Hq / Hkv <= 128, B <= 1024,
+ * included).  A sequence's own K and V must be finite: one that is not may reach
+ * queries that its window or causality keeps it from.  Requires D in {64, 128}, Hq / Hkv <= 128, B <= 1024,
  * max_pages_per_seq * page_size <= 2^30, num_pages * page_size < 2^31.
  */
 WPATTN_API int wpattn_prefill_paged(const wpattn_window *w,

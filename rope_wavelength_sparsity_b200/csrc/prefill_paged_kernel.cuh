@@ -28,9 +28,20 @@
 //              the page, up to 128).  One warp issues a copy every 40-54 ns,
 //              whatever its size; 16-key pages need 16 a step, so K and V have
 //              a warp each.
-//   warps 9, 10  MMA issuers of tile 0 / 1 (one alone was the bound: its issue
-//              and waits took 3900 cycles a step); warp 9 owns the TMEM.
+//   warps 9, 10  MMA issuers of tile 0 / 1; warp 9 owns the TMEM.  They issue as
+//              whole warps, see warp_mma_ss.
 //   The V producer also zeroes the V rows behind the sequence's last key.
+//
+// What bounds it.  A two-tile step is 2 x (QK + PV): 2070 tensor cycles at D =
+// 128, and 2048 of the SM's exponentials, at 16 a clock.  A tile's chain is
+// longer than either: its scores' way to registers and their maximum (450
+// cycles), 128 exponentials a thread (1350 alone, 2240 when both tiles'
+// warps of an SM partition are at theirs), P's hand-over, the last quarter of
+// PV and the next QK (1150; at D = 64 that QK runs early, beside the softmax).
+// Measured: 3650 cycles a step at D = 128, 3150 at D = 64 (4100 and 3700 with
+// the tiles' exponentials side by side).  4096 queries of 28 heads on 128K keys,
+// 4 kv heads, g = 8: 5.55 ms, 1027 TFLOP/s of kept terms; one query a
+// sequence: 7.0 TB/s of K and V.
 //
 // Shared-memory layouts.  K and V tiles are groups of 8 keys, each D / 64
 // panels of 8 rows x 128 bytes, 128-byte swizzled: the layout one 4-D copy
@@ -41,11 +52,10 @@
 // half, and a unit of 16 pairs is two steps.  Q is no-swizzle K-major:
 // 16-byte columns of 128 rows, 2 KB apart.
 //
-// TMEM columns: each tile has two score buffers of 64 keys, 64 columns wide, at
-// 128 t (P, bf16, over the first half of each), so that the scores of a key
-// tile are computed while the softmax works on the one before it: with one
-// buffer a step was the sum of its softmax and of its products (4400 cycles
-// for 128 keys; exponentials alone take 2048, products 2100).  O_t at 256 + t D.
+// TMEM columns: S_t at 128 t, O_t at 256 + t D; P_t (bf16) over the first half of
+// S_t at D = 128, at 384 + 64 t at D = 64.  (Two score buffers of 64 keys per
+// tile, which fit at D = 128 too and take QK off a tile's chain, were slower,
+// 2.7 us a step: what a step costs beside its exponentials doubles.)
 #pragma once
 
 #include <type_traits>
@@ -693,8 +703,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
               }
             }
           } else {
-            // One pair is two products an element, on the FMA pipe: as an MMA with all
-            // but the pair's own dims zeroed it took twice as long.
+            // One pair is two products an element, on the FMA pipe.  (As MMAs with all
+            // but the pair's own dims zeroed, and the pairs searched one by one, a
+            // tile on the diagonal took 9.9 us more than a plain one, now 6.2 us.)
             const int c0 = 2 * (lane & 3);     // this lane's columns: c0 and c0 + 1 of each 8
 #pragma unroll 1
             for (int pp = pa; pp < pb; ++pp) {
