@@ -169,7 +169,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
 }
 
 // This block's share of a copy of 16-byte units: four loads ahead of their stores
-// (compaction of 1965 pages of 64 KB in 4 pools: 174 us, 6.0 TB/s read and
+// (compaction of 1965 pages of 64 KB in 4 pools: 174 us, 5.9 TB/s read and
 // written; one load at a time and whole pages per block 208 us).
 __device__ __forceinline__ void block_copy(uint8_t* __restrict__ dst, const uint8_t* __restrict__ src, int64_t units) {
   uint4* d = reinterpret_cast<uint4*>(dst);
