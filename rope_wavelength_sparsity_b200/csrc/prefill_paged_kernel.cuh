@@ -58,8 +58,6 @@
 // 2.7 us a step: what a step costs beside its exponentials doubles.)
 #pragma once
 
-#include <type_traits>
-
 #include "device_util.cuh"
 #include "prefill_kernel.cuh"
 
@@ -615,19 +613,18 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       if (r == 0) sPS[t] = plan_next & 0xFFFF;
     };
     const float sl = p.scale_log2;
-    // Step j, its scores in S: from there to P's hand-over.  Most steps are plain:
-    // no correction, no key masked, not every pair pruned.  They have code of
-    // their own, in one piece; with the other cases' branches in it the
-    // same step took 800 cycles more.
-    auto step = [&](auto is_special, int j, int plan, int plan_next, bool more) {
-      constexpr bool SPECIAL = decltype(is_special)::value;
+    // What a step that is not plain changes in S before the softmax reads it: scores
+    // corrected, keys masked, every pair pruned.  In TMEM, in code of its own and in
+    // loops: with these branches in the softmax's code every step took 800
+    // cycles more, and a second copy of that code for them 2 us of a cold start.
+    auto prepare_scores = [&](int j, int plan) {
       const int kp0 = KT * (top - j);
       const int d_row = i_pos - kp0;           // distance to the tile's first key
       // Per-element corrections, d = d_row - c for column c of the tile:
       // pairs plo .. ps - 1 were left out: add them where 0 <= d <= T;
       // pairs ps .. P - 1 were contracted: subtract them where d > T.
       const int plo = plan >> 16, ps = plan & 0xFF;
-      if (SPECIAL && (plan & kCorr)) {
+      if (plan & kCorr) {
         const int sk = j % NSK;
         const bool need_sub = __any_sync(FULL, d_row > sT[min(ps, P - 1)]);
         const int T_add = ps > plo ? sT[ps - 1] : -1;
@@ -757,6 +754,23 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         if (lane == 0 && (atomicAdd(reinterpret_cast<int*>(smem + L::OFF_LEFT) + t, 1) & 3) == 3)
           mbar_arrive(k_empty(sk));
       }
+      // causal mask (d < 0) and the sequence's end: columns c > cm; every pair pruned: score 0
+      const int cm = min(d_row, it.kv_len - 1 - kp0);
+#pragma unroll 1
+      for (int cc = 0; cc < KT / 32; ++cc) {
+        if (plo < P && __all_sync(FULL, cm >= 32 * cc + 31)) continue;
+        float v[32];
+        tmem_ld32(tS + 32 * cc, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = 32 * cc + c > cm ? -INFINITY : plo >= P ? 0.f : v[c];
+        tmem_st32(tS + 32 * cc, v);
+      }
+      tmem_st_wait();
+    };
+    // Step j, its scores in S: from there to P's hand-over.
+    auto step = [&](int j, int plan, int plan_next, bool more) {
+      if (plan & kSpecial) prepare_scores(j, plan);
       float sc[KT];
 #pragma unroll
       for (int cc = 0; cc < KT / 32; ++cc) tmem_ld32(tS + 32 * cc, &sc[32 * cc]);
@@ -770,17 +784,6 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       // the loaded values are only defined after the wait: keep every use below it
 #pragma unroll
       for (int c = 0; c < KT; ++c) asm volatile("" : "+f"(sc[c]));
-      if (SPECIAL && plo >= P) {
-#pragma unroll
-        for (int c = 0; c < KT; ++c) sc[c] = 0.f;   // every pair pruned: score 0
-      }
-      // causal mask (d < 0) and the sequence's end: columns c > cm
-      if (SPECIAL) {
-        const int cm = min(max(min(d_row, it.kv_len - 1 - kp0), -1), KT);
-#pragma unroll
-        for (int c = 0; c < KT; ++c)
-          if (c > cm) sc[c] = -INFINITY;
-      }
       // row max, then the exponentials against the (lazily moved) reference
       float mt;
       {
@@ -864,8 +867,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       else if (more) plan_next = plan_step(j + stride);
       if (!__all_sync(FULL, mbar_wait_handoff(s_full(t), cnt & 1))) { ok = false; break; }
       tc_fence_after();
-      if (plan & kSpecial) step(std::true_type{}, j, plan, plan_next, more);
-      else step(std::false_type{}, j, plan, plan_next, more);
+      step(j, plan, plan_next, more);
       ++cnt;
       plan = plan_next;
     }
