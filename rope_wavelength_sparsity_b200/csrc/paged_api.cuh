@@ -347,8 +347,17 @@ int launch_paged(const PagedCall& c) {
   kernel<<<c.plan.ctas, 384, L::ALLOC, c.st>>>(maps[0], maps[1], p);
   const int rc = launched();
   if (rc != WPATTN_OK || c.plan.split_ctas == 0) return rc;
-  prefill_paged_merge_kernel<D, MAXB><<<dim3(c.plan.split_ctas, D / 32), 256, 0, c.st>>>(p);
-  return launched();
+  // launched while the parts' kernel runs; it waits for that kernel's end by itself
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.plan.split_ctas, D / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = c.st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_paged_merge_kernel<D, MAXB>, p) == cudaSuccess ? launched() : WPATTN_ECUDA;
 }
 
 template <int D, bool G8>

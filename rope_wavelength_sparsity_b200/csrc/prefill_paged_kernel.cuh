@@ -274,6 +274,8 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   volatile int* sPS = reinterpret_cast<volatile int*>(smem + L::OFF_PS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM);
 
+  // the merge kernel may take its place on an SM as soon as there is room
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the swizzled tiles need a 1024-byte aligned shared window
   if (sbase & 1023u) {
     if (threadIdx.x == 0) record_status(2 /* WPATTN_EUNSUPPORTED */);
@@ -965,6 +967,7 @@ prefill_paged_merge_kernel(const __grid_constant__ PrefillPagedParams<MAXB> p) {
   const int c = blockIdx.x;
   const PagedItem it = paged_item(p, c);
   if (it.part != 0) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are there (the kernel before has ended)
   const int t = threadIdx.x >> 7, r = threadIdx.x & 127;
   const int tok = r / p.G;
   if ((it.dup && t == 1) || r >= p.tile_tokens * p.G || tok >= it.ntok[t]) return;
