@@ -33,13 +33,13 @@
 //   The V producer also zeroes the V rows behind the sequence's last key.
 //
 // What bounds it.  A two-tile step is 2 x (QK + PV): 2070 tensor cycles at D =
-// 128, and 2048 of the SM's exponentials, at 16 a clock.  A tile's chain is
-// longer than either: its scores' way to registers and their maximum (450
-// cycles), 128 exponentials a thread (1350 alone, 2240 when both tiles'
+// 128, and 2048 of the SM's exponentials, at 16 a clock.  At D = 128 a tile's
+// chain is longer than either: its scores' way to registers and their maximum
+// (450 cycles), 128 exponentials a thread (1350 alone, 2240 when both tiles'
 // warps of an SM partition are at theirs), P's hand-over, the last quarter of
-// PV and the next QK (1150; at D = 64 that QK runs early, beside the softmax).
-// Measured: 3650 cycles a step at D = 128, 3150 at D = 64 (4100 and 3700 with
-// the tiles' exponentials side by side).  4096 queries of 28 heads on 128K keys,
+// PV and the next QK (1150).  Measured: 3650 cycles a step (4100 with the
+// tiles' exponentials side by side).  At D = 64 the next QK runs early, beside
+// the softmax, and a step is both tiles' softmax passes: 3000 cycles.  4096 queries of 28 heads on 128K keys,
 // 4 kv heads, g = 8: 5.55 ms, 1027 TFLOP/s of kept terms; one query a
 // sequence: 7.0 TB/s of K and V.
 //
@@ -250,7 +250,9 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   // D = 64 leaves 128 TMEM columns free: P has columns of its own, and the next
   // QK starts as soon as the softmax group has its scores in registers
   constexpr bool EARLY = D == 64;
-  constexpr int kMost = KT * 3 / 4;     // keys of P's first hand-over
+  // keys of P's first hand-over: at D = 128 most of PV runs under the last
+  // exponentials; where PV is off the tile's chain the stores' wait costs more
+  constexpr int kMost = EARLY ? 0 : KT * 3 / 4;
   constexpr int kCorr = 1 << 8, kSpecial = 1 << 9;   // of a step's plan, beside its split pair
   constexpr uint32_t FULL = 0xffffffffu;
 
@@ -469,9 +471,8 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         ok = __all_sync(FULL, mbar_wait_handoff(v_full(sv), pv));
         if (tail && n == 0 && j0 == 0) ok = ok && __all_sync(FULL, mbar_wait(v_fix, 0));
         const uint32_t va = v_lo | ((sbase + L::OFF_V + sv * TILE) >> 4);
-        // most of P's product runs under its last exponentials
 #pragma unroll
-        for (int last = 0; last < 2; ++last) {
+        for (int last = kMost ? 0 : 1; last < 2; ++last) {
           ok = ok && __all_sync(FULL, mbar_wait_handoff(last ? p_full(t) : p_most(t), n & 1));
           if (!ok) break;
           tc_fence_after();
@@ -824,13 +825,17 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       // p, rounded to bf16 (the MMA's operand type); l sums them unrounded
       {
         float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
-        // Warps w and w + 4 share an SM partition and its exponentials.  They take
-        // turns, tile 0 first in each step, so that one tile's other work runs
-        // under the other's exponentials (side by side both would wait for both),
-        // in the same order on every partition (or a tile waits for its last
-        // warp).  The wait is bounded and may be given up: it orders nothing.
+        if constexpr (!EARLY) {
+          // Warps w and w + 4 share an SM partition and its exponentials.  They take
+          // turns, tile 0 first in each step, so that one tile's products run under
+          // the other's exponentials (side by side both would wait for both), in
+          // the same order on every partition (or a tile waits for its last
+          // warp).  The wait is bounded and may be given up: it orders nothing.
+          // At D = 64, whose next QK is early, side by side is faster: 1.57 us a step
+          // against 1.65.
 #pragma unroll 1
-        for (int i = 0; i < 256 && turn[warp ^ 4] < (t && !dup ? j + 1 : j); ++i) {}
+          for (int i = 0; i < 256 && turn[warp ^ 4] < (t && !dup ? j + 1 : j); ++i) {}
+        }
         asm volatile("" : "+f"(nm));           // no exponential above this
         float acc[8];
 #pragma unroll
@@ -843,18 +848,23 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
           add2(acc[2 * (i & 3)], acc[2 * (i & 3) + 1], acc[2 * (i & 3)], acc[2 * (i & 3) + 1], e0, e1);
           pk2[i] = pack_bf16x2(e0, e1);
-          if (i == kMost / 2 - 1) {
+          if (kMost && i == kMost / 2 - 1) {
             tmem_st32u(tP, pk2);
             tmem_st16u(tP + 32, pk2 + 32);
-            if (!EARLY && more) tell_next(plan, plan_next);
+            if (more) tell_next(plan, plan_next);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_most(t));
           }
         }
-        tmem_st16u(tP + 48, pk2 + 48);
-        if (lane == 0) turn[warp] = j + 1;
+        if constexpr (EARLY) {
+          tmem_st32u(tP, pk2);
+          tmem_st32u(tP + 32, pk2 + 32);
+        } else {
+          tmem_st16u(tP + 48, pk2 + 48);
+          if (lane == 0) turn[warp] = j + 1;
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
