@@ -36,11 +36,11 @@ int launch_rope_axes(AxesParams<MAXB>& p, int D, int num_sms, cudaStream_t st) {
   return launched();
 }
 
-// arguments that the rotating entry points share
+// arguments that the rotating entry points share (positions of no token may be NULL, as an empty tensor's are)
 bool axes_ok(int D, int64_t tokens, const int32_t* positions, int64_t pos_stride, int32_t axes,
              const uint8_t* pair_axis, double base) {
   if (!(base > 1.0) || std::isinf(base) || axes < 1 || axes > kMaxAxes) return false;
-  if (!positions && axes != 1) return false;
+  if (!positions && axes != 1 && tokens > 0) return false;
   if (positions && (!aligned4(positions) || (axes > 1 && pos_stride < tokens))) return false;
   for (int i = 0; pair_axis && i < D / 2; ++i)
     if (pair_axis[i] >= axes) return false;
@@ -378,7 +378,7 @@ int wpattn_rope_axes(const void* q, int64_t q_stride, void* q_out, const void* k
                      double rope_base, int32_t inverse, void* cuda_stream) {
   if (tokens < 0 || Hq <= 0 || (k && Hkv <= 0) || (!k != !k_out)) return WPATTN_EINVAL;
   if (head_dim != 64 && head_dim != 128) return WPATTN_EUNSUPPORTED;
-  if (!positions || (inverse != 0 && inverse != 1) ||
+  if ((!positions && tokens > 0) || (inverse != 0 && inverse != 1) ||
       !axes_ok(head_dim, tokens, positions, pos_stride, axes, pair_axis_host, rope_base))
     return WPATTN_EINVAL;
   if (tokens == 0) return WPATTN_OK;

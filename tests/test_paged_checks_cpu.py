@@ -82,6 +82,13 @@ def test_append_paged_refusals(kw, code):
     assert _append(**kw) == getattr(wp, code)
 
 
+def test_positions_of_no_token_may_be_null():
+    """What an empty [axes, 0] tensor passes."""
+    assert _rope(T=0, q=None, qo=None, k=None, ko=None, pos=None, stride=0, axes=3) == wp.OK
+    assert _append(new=_i(0, 0), pos=None, axes=3) == wp.OK
+    assert _append(new=_i(0, 1), pos=None, axes=3) == wp.EINVAL
+
+
 def test_page_operator_refusals():
     L = wp.lib()
     ok = wp.EINVAL, wp.EUNSUPPORTED
