@@ -39,9 +39,9 @@
 // warps of an SM partition are at theirs), P's hand-over, the last quarter of
 // PV and the next QK (1150).  Measured: 3650 cycles a step (4100 with the
 // tiles' exponentials side by side).  At D = 64 the next QK runs early, beside
-// the softmax, and a step is both tiles' softmax passes: 3000 cycles.  4096 queries of 28 heads on 128K keys,
-// 4 kv heads, g = 8: 5.55 ms, 1027 TFLOP/s of kept terms; one query a
-// sequence: 7.0 TB/s of K and V.
+// the softmax, and a step is both tiles' softmax passes: 3000 cycles.  4096
+// queries of 28 heads on 128K keys, 4 kv heads, g = 8: 5.55 to 5.9 ms, about
+// 1000 TFLOP/s of kept terms; one query a sequence: 7.0 TB/s of K and V.
 //
 // Shared-memory layouts.  K and V tiles are groups of 8 keys, each D / 64
 // panels of 8 rows x 128 bytes, 128-byte swizzled: the layout one 4-D copy
@@ -920,7 +920,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         l_run = l_run * w0 + other.y * w1;
         m_ref = M;
       }
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;   // a NaN stays one, in O and in the parts
       w0 *= inv;
       w1 *= inv;
       const bool both = dup && steps > 1;      // group 1 had a key tile
@@ -955,7 +955,7 @@ prefill_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
                            pack_bf16x2(o[8 * c8 + 4], o[8 * c8 + 5]), pack_bf16x2(o[8 * c8 + 6], o[8 * c8 + 7]));
         }
       }
-      const float l2 = l_run > 0.f ? m_ref + __log2f(l_run) : -INFINITY;
+      const float l2 = l_run != 0.f ? m_ref + __log2f(l_run) : -INFINITY;
       if (row_ok && split) p.part_l[prow] = l2;
       else if (row_ok && p.lse) p.lse[qrow] = l2 * 0.69314718055994530942f;
     }
@@ -1004,7 +1004,7 @@ prefill_paged_merge_kernel(const __grid_constant__ PrefillPagedParams<MAXB> p) {
       for (int e = 0; e < 8; ++e) acc[8 * e8 + e] = fmaf(w, v[e], acc[8 * e8 + e]);
     }
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = W != 0.f ? 1.f / W : 0.f;
   const size_t row = (static_cast<size_t>(it.row0) + it.tok[t] + tok) * p.Hq + static_cast<size_t>(it.kvh) * p.G + r % p.G;
   uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + 32 * blockIdx.y);
 #pragma unroll
@@ -1013,7 +1013,7 @@ prefill_paged_merge_kernel(const __grid_constant__ PrefillPagedParams<MAXB> p) {
     dst[e8] = make_uint4(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv),
                          pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
   }
-  if (p.lse && blockIdx.y == 0) p.lse[row] = W > 0.f ? (M + __log2f(W)) * 0.69314718055994530942f : -INFINITY;
+  if (p.lse && blockIdx.y == 0) p.lse[row] = W != 0.f ? (M + __log2f(W)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace wpattn

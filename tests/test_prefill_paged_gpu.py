@@ -142,6 +142,26 @@ def test_agrees_with_contiguous_prefill_and_paged_decode(cuda_dev):
     assert (lse[last] - dec_lse).abs().max() <= 1e-4
 
 
+@pytest.mark.parametrize("name", ["two_tiles", "long_chunk_g8", "drafts", "long_context", "long_context_chunk"])
+def test_nan_in_a_query_row_stays_there(cuda_dev, name):
+    """The row comes out as NaN (also where its keys are split), every other as without it."""
+    D, g, alpha, base, Hq, Hkv, page, q_len, kv_len = CASES[name]
+    kp, vp, table, _, _ = make_cache(kv_len, page, Hkv, D, 21)
+    q = torch.randn((sum(q_len), Hq, D), generator=torch.Generator().manual_seed(22)).to(torch.bfloat16).cuda()
+    win = wp.Window(D, base, alpha, g)
+    want, want_lse = wp.prefill_paged(q, kp, vp, table, q_len, kv_len, win)
+    rows = {(0, 0), (sum(q_len) // 2, Hq - 1), (sum(q_len) - 1, Hq // 2)}
+    for t, h in rows:
+        q[t, h, D // 2 - 1] = float("nan")
+    out, lse = wp.prefill_paged(q, kp, vp, table, q_len, kv_len, win)
+    hit = torch.zeros((sum(q_len), Hq), dtype=torch.bool, device="cuda")
+    for t, h in rows:
+        hit[t, h] = True
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    assert wp.device_status() == wp.OK
+
+
 def test_rows_far_into_a_large_pool(cuda_dev):
     """Pages whose byte offset passes 2^31 and whose element offset passes 2^31."""
     D, Hkv, page = 128, 8, 128
