@@ -599,8 +599,9 @@ WPATTN_API int wpattn_append_paged(const void *k, int64_t k_stride,
  * (a multiple of 16) in each.  Only full pages are shared between rows, so
  * a sequence always owns the page it appends to.  Free pages are taken lowest
  * index first: results do not depend on timing.  Calls on one cache are
- * ordered by its stream; at most 1024 rows per call.  Rows named twice, rows
- * outside the table and lengths outside it are WPATTN_EINVAL.
+ * ordered by its stream; at most 1024 rows per call, 2^30 pages, max_pages *
+ * page_size <= 2^30 (else WPATTN_EUNSUPPORTED).  Rows named twice, rows outside
+ * the table and lengths outside it are WPATTN_EINVAL.
  *
  * wpattn_pages_copy: page src[i] of every pool onto page dst[i], i < n (device
  * int32 [n] each).  No page may be written that the call also reads or writes

@@ -70,6 +70,11 @@ int set_pools(PagePools* out, void* const* pools, int32_t n_pools, int64_t page_
   return WPATTN_OK;
 }
 
+// what the page kernels' 32-bit loops and the rounding up to whole pages can take
+bool page_counts_ok(int32_t num_pages, int32_t page_size, int32_t max_pages) {
+  return num_pages <= (1 << 30) && int64_t(max_pages) * page_size <= (int64_t(1) << 30);
+}
+
 // 1 <= n <= kPageRows rows named once each, inside the table; sorted into `sorted`
 bool rows_ok(const int32_t* rows, int32_t n, int32_t num_rows, int32_t (&sorted)[kPageRows]) {
   std::copy(rows, rows + n, sorted);
@@ -500,6 +505,7 @@ int wpattn_pages_copy(void* const* pools_host, int32_t n_pools, int32_t num_page
   int rc = set_pools(&p.pools, pools_host, n_pools, page_bytes);
   if (rc != WPATTN_OK) return rc;
   if (n < 0 || num_pages <= 0) return WPATTN_EINVAL;
+  if (n > (1 << 30)) return WPATTN_EUNSUPPORTED;
   if (n == 0 || n_pools == 0) return WPATTN_OK;
   if (!src || !dst || !aligned4(src) || !aligned4(dst)) return WPATTN_EINVAL;
   DeviceInfo* dev = nullptr;
@@ -524,7 +530,7 @@ int wpattn_pages_fork(void* const* pools_host, int32_t n_pools, int32_t num_page
   int rc = set_pools(&pools, pools_host, n_pools, row_bytes * page_size);
   if (rc != WPATTN_OK) return rc;
   if (n < 0 || num_pages <= 0 || num_rows <= 0 || max_pages <= 0) return WPATTN_EINVAL;
-  if (n > kPageRows) return WPATTN_EUNSUPPORTED;
+  if (n > kPageRows || !page_counts_ok(num_pages, page_size, max_pages)) return WPATTN_EUNSUPPORTED;
   if (n == 0) return WPATTN_OK;
   if (!block_table || !refs || !src_rows_host || !dst_rows_host || !len_host || !aligned4(block_table) ||
       !aligned4(refs))
@@ -548,7 +554,7 @@ int wpattn_pages_free(int32_t num_pages, int32_t page_size, int32_t* block_table
                       int32_t max_pages, int32_t* refs, const int32_t* rows_host, const int32_t* len_host,
                       int32_t n, void* cuda_stream) {
   if (n < 0 || num_pages <= 0 || page_size <= 0 || num_rows <= 0 || max_pages <= 0) return WPATTN_EINVAL;
-  if (n > kPageRows) return WPATTN_EUNSUPPORTED;
+  if (n > kPageRows || !page_counts_ok(num_pages, page_size, max_pages)) return WPATTN_EUNSUPPORTED;
   if (n == 0) return WPATTN_OK;
   int32_t sorted[kPageRows];
   if (!block_table || !refs || !rows_host || !len_host || !aligned4(block_table) || !aligned4(refs) ||
@@ -572,7 +578,7 @@ int wpattn_pages_extend(int32_t num_pages, int32_t page_size, int32_t* block_tab
                         int32_t max_pages, int32_t* refs, const int32_t* rows_host, const int32_t* len_host,
                         const int32_t* new_len_host, int32_t n, void* cuda_stream) {
   if (n < 0 || num_pages <= 0 || page_size <= 0 || num_rows <= 0 || max_pages <= 0) return WPATTN_EINVAL;
-  if (n > kPageRows) return WPATTN_EUNSUPPORTED;
+  if (n > kPageRows || !page_counts_ok(num_pages, page_size, max_pages)) return WPATTN_EUNSUPPORTED;
   if (n == 0) return WPATTN_OK;
   int32_t sorted[kPageRows];
   if (!block_table || !refs || !rows_host || !len_host || !new_len_host || !aligned4(block_table) ||
@@ -609,6 +615,7 @@ int wpattn_pages_compact(void* const* pools_host, int32_t n_pools, int32_t num_p
   if (num_pages <= 0 || entries < 0 || (entries > 0 && !block_table) || !refs || !aligned4(block_table) ||
       !aligned4(refs) || !aligned4(live))
     return WPATTN_EINVAL;
+  if (num_pages > (1 << 30)) return WPATTN_EUNSUPPORTED;
   if (!workspace || workspace_bytes < wpattn_pages_workspace_size(num_pages)) return WPATTN_EWORKSPACE;
   if (!aligned16(workspace)) return WPATTN_EINVAL;
   DeviceInfo* dev = nullptr;

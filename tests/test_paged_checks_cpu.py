@@ -89,6 +89,23 @@ def test_positions_of_no_token_may_be_null():
     assert _append(new=_i(0, 1), pos=None, axes=3) == wp.EINVAL
 
 
+def test_page_operator_sizes():
+    """At most 2^30 pages and 2^30 keys a row: no index of the kernels passes 32 bits."""
+    L, big = wp.lib(), 2**31 - 1
+
+    def calls(num_pages, page, width, length):
+        n = L.wpattn_pages_workspace_size(num_pages)
+        yield L.wpattn_pages_fork(_p(256), 1, num_pages, page, 32, V, 6, width, V, _i(0), _i(1), _i(length), 1, V, n, None)
+        yield L.wpattn_pages_free(num_pages, page, V, 6, width, V, _i(0), _i(length), 1, None)
+        yield L.wpattn_pages_extend(num_pages, page, V, 6, width, V, _i(0), _i(0), _i(length), 1, None)
+
+    for args in [(big, 16, 3, 40), (8, 16, big, big), (8, 16, 1 << 27, 40), (8, big, 1, big), (8, big, 2, 7)]:
+        assert set(calls(*args)) == {wp.EUNSUPPORTED}, args
+    n = L.wpattn_pages_workspace_size(big)
+    assert L.wpattn_pages_compact(_p(256), 1, big, 32, V, 12, V, V, V, n, None) == wp.EUNSUPPORTED
+    assert L.wpattn_pages_copy(_p(256), 1, 8, 32, V, V, big, None) == wp.EUNSUPPORTED
+
+
 def test_page_operator_refusals():
     L = wp.lib()
     ok = wp.EINVAL, wp.EUNSUPPORTED
