@@ -275,6 +275,29 @@ def test_compact_any_pool(cuda_dev, num_pages, used):
     assert wp.device_status() == wp.OK
 
 
+def test_a_thousand_rows(cuda_dev):
+    """As many rows as a call takes: grown, forked (many from one source), freed again."""
+    page, rows = 8, 1034
+    made, table, refs, host = _cache(page, 1, 64, 2, 3000, rows, 4)
+    src_len = [1 + 3 * i for i in range(10)]
+    wp.pages_extend(table, refs, range(10), [0] * 10, src_len, page)
+    host.extend(range(10), [0] * 10, src_len)
+    dst = list(range(10, rows))
+    src = [i * i % 10 for i in range(1024)]
+    ln = [src_len[r] - i % 2 for i, r in enumerate(src)]
+    wp.pages_fork(made, table, refs, src, dst, ln)
+    host.fork(src, dst, ln)
+    host.check(made, table, refs)
+    new = [n + i % 5 for i, n in enumerate(ln)]
+    wp.pages_extend(table, refs, dst, ln, new, page)
+    host.extend(dst, ln, new)
+    host.check(made, table, refs)
+    wp.pages_free(table, refs, dst, new, page)
+    host.free(dst, new)
+    host.check(made, table, refs)
+    assert wp.device_status() == wp.OK and int(refs.sum()) == sum(pages_of(n, page) for n in src_len)
+
+
 def test_too_few_pages(cuda_dev):
     made, table, refs, host = _cache(8, 1, 64, 2, 5, 6, 4)
     wp.pages_extend(table, refs, [0, 1], [0, 0], [20, 9], 8)      # 3 + 2 of 5 pages

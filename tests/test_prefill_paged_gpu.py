@@ -35,6 +35,8 @@ CASES = {
     "many_drafts": (64, 8, 1.0, 1e6, 8, 2, 32, [3] * 80, [1500 - 11 * i for i in range(80)]),
     "long_context": (64, 1, 1.0, 1e6, 4, 2, 16, [2, 1], [20000, 9001]),
     "long_context_chunk": (128, 8, 1.0, 1e7, 7, 1, 64, [150], [12000]),
+    "million_keys": (64, 8, 1.0, 1e7, 2, 1, 256, [3], [(1 << 20) + 5]),
+    "most_sequences": (128, 8, 1.0, 1e4, 2, 1, 8, [i % 4 for i in range(1024)], [1 + i % 97 for i in range(1024)]),
 }
 
 
