@@ -593,7 +593,7 @@ int wpattn_pages_extend(int32_t num_pages, int32_t page_size, int32_t* block_tab
     p.row[i] = rows_host[i];
     p.first[i] = (len_host[i] + page_size - 1) / page_size;
     want += (new_len_host[i] + page_size - 1) / page_size - p.first[i];
-    if (want > INT32_MAX) return WPATTN_EUNSUPPORTED;
+    if (want > (1 << 30)) return WPATTN_EUNSUPPORTED;   // the kernel's loops step past it by a block of threads
     p.start[i + 1] = static_cast<int>(want);
   }
   if (want == 0) return WPATTN_OK;
