@@ -520,7 +520,7 @@ WPATTN_API int wpattn_merge_lse(const void *outs, const float *lses, int32_t R, 
  * Rows of the pools behind a sequence's last key hold anything (NaN
  * included).  A sequence's own K and V must be finite: one that is not may reach
  * queries that its window or causality keeps it from.  Requires D in {64, 128}, Hq / Hkv <= 128, B <= 1024,
- * max_pages_per_seq * page_size <= 2^30, num_pages * page_size < 2^31.
+ * T < 2^31 - 127, max_pages_per_seq * page_size <= 2^30, num_pages * page_size < 2^31.
  */
 WPATTN_API int wpattn_prefill_paged(const wpattn_window *w,
                   const void *q, const void *k_pages, const void *v_pages,

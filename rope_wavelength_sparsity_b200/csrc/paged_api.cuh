@@ -120,6 +120,9 @@ int64_t sum_lengths(const int32_t* len, int32_t B) {
   return sum <= INT32_MAX ? sum : -1;
 }
 
+// tokens of a prefill: rounded up to whole row tiles (of at most 128) they still fit 32 bits
+constexpr int64_t kMaxTokens = INT32_MAX - 127;
+
 template <int MAXN>
 int launch_fork(const PagePools& pools, int num_pages, int page_size, int64_t row_bytes, int32_t* table,
                 int max_pages, int32_t* refs, const int32_t* src, const int32_t* dst, const int32_t* len, int n,
@@ -447,7 +450,8 @@ size_t wpattn_prefill_paged_workspace_size(const wpattn_window* w, const int32_t
   if (make_window_plan(w, &plan) != WPATTN_OK || (plan.D != 64 && plan.D != 128)) return 0;
   if (B <= 0 || B > kPagedMaxB || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 128 || !q_len_host || !kv_len_host)
     return 0;
-  if (sum_lengths(q_len_host, B) < 0) return 0;
+  const int64_t tokens = sum_lengths(q_len_host, B);
+  if (tokens < 0 || tokens > kMaxTokens) return 0;
   for (int b = 0; b < B; ++b)
     if (kv_len_host[b] < 0 || kv_len_host[b] > (1 << 30)) return 0;
   DeviceInfo* dev = nullptr;
@@ -479,7 +483,9 @@ int wpattn_prefill_paged(const wpattn_window* w, const void* q, const void* k_pa
   if (!q || !out || !k_pages || !v_pages || !block_table || !aligned4(block_table) || !aligned4(lse))
     return WPATTN_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(k_pages) || !aligned16(v_pages)) return WPATTN_EINVAL;
-  if (cap > (int64_t(1) << 30) || int64_t(num_pages) * page_size >= (int64_t(1) << 31)) return WPATTN_EUNSUPPORTED;
+  if (cap > (int64_t(1) << 30) || int64_t(num_pages) * page_size >= (int64_t(1) << 31) ||
+      tokens > kMaxTokens)
+    return WPATTN_EUNSUPPORTED;
   PagedCall c;
   if ((rc = device_info(&c.dev)) != WPATTN_OK) return rc;
   if (!plan_paged(q_len_host, kv_len_host, B, Hq / Hkv, Hkv, plan, c.dev->num_sms, &c.plan))
