@@ -641,9 +641,13 @@ WPATTN_API int wpattn_pages_free(int32_t num_pages, int32_t page_size,
 
 /*
  * Row i grows from len[i] to new_len[i] keys: the pages it lacks are the lowest
- * free ones, row by row.  Without enough of them the last entries stay -1
- * and WPATTN_EPAGES is recorded.  At most 2^30 new pages per call, all rows
- * together (else WPATTN_EUNSUPPORTED).
+ * free ones, row by row.  An entry behind len[i] that names a page in use keeps
+ * it: a row that was cut back (drafts that were not kept) grows into the pages
+ * it holds.  (One that names a free page is replaced, and WPATTN_EINDEX
+ * recorded.)  Cutting back is the host's: a smaller length, though not below one
+ * that the row was forked at, since pages behind that may be shared.  Without
+ * enough free pages the last entries stay -1 and WPATTN_EPAGES is recorded.  At
+ * most 2^30 entries per call, all rows together (else WPATTN_EUNSUPPORTED).
  */
 WPATTN_API int wpattn_pages_extend(int32_t num_pages, int32_t page_size,
                   int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *refs,

@@ -284,31 +284,48 @@ struct ExtendParams {
   int32_t* refs;
   int num_pages, max_pages, n;
   int row[kPageRows], first[kPageRows];   // table row, its first new entry
-  int start[kPageRows + 1];               // rank of that entry among the call's new pages
+  int start[kPageRows + 1];               // rank of that entry among the call's
 };
 
-// Rank r among the call's new pages gets the r-th lowest free page.
+// The entries that lack a page get the lowest free ones, in their order.  One that names
+// a page in use keeps it: the row holds more pages than its length needs (drafts
+// that were not kept).  A thread per entry finds those that lack one, 1024 at a
+// time; then the pool's refs go by, from where the entries before left them.
 __global__ void __launch_bounds__(kScanThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
   __shared__ int sums[kScanThreads / 32];
+  __shared__ int32_t* slots[kScanThreads];   // the entries that lack a page
   const int want = p.start[p.n];
-  auto put = [&](int rank, int page) {
-    const int i = find_sequence(p.start, p.n, rank);
-    p.table[static_cast<int64_t>(p.row[i]) * p.max_pages + p.first[i] + rank - p.start[i]] = page;
-  };
-  int found = 0;
-  for (int base = 0; base < p.num_pages && found < want; base += kScanThreads) {
-    const int i = base + threadIdx.x;
-    const int mine = i < p.num_pages && p.refs[i] == 0 ? 1 : 0;
-    int total;
-    const int at = found + block_scan(mine, sums, &total);
-    if (mine && at < want) {
-      p.refs[i] = 1;
-      put(at, i);
+  int base = 0;                              // every page before it is in use
+  for (int r0 = 0; r0 < want; r0 += kScanThreads) {
+    const int r = r0 + threadIdx.x;
+    int32_t* entry = nullptr;
+    int lacks = 0, n = 0, got = 0;
+    if (r < want) {
+      const int i = find_sequence(p.start, p.n, r);
+      entry = p.table + static_cast<int64_t>(p.row[i]) * p.max_pages + p.first[i] + r - p.start[i];
+      const int e = *entry;
+      lacks = e < 0 || e >= p.num_pages || p.refs[e] <= 0 ? 1 : 0;
+      if (lacks && e >= 0 && e < p.num_pages) record_status(6 /* WPATTN_EINDEX */);   // a free page
     }
-    found += total;
+    const int at = block_scan(lacks, sums, &n);
+    if (lacks) slots[at] = entry;
+    __syncthreads();
+    while (got < n && base < p.num_pages) {
+      const int i = base + threadIdx.x;
+      const int mine = i < p.num_pages && p.refs[i] == 0 ? 1 : 0;
+      int found;
+      const int k = got + block_scan(mine, sums, &found);
+      if (mine && k < n) {
+        p.refs[i] = 1;
+        *slots[k] = i;
+      }
+      if (got + found <= n) base += kScanThreads;   // else the next entries take the rest of these
+      got = min(got + found, n);
+    }
+    if (got < n && threadIdx.x == 0) record_status(7 /* WPATTN_EPAGES */);
+    for (int k = got + threadIdx.x; k < n; k += kScanThreads) *slots[k] = -1;
+    __syncthreads();                         // slots may be reused
   }
-  if (found < want && threadIdx.x == 0) record_status(7 /* WPATTN_EPAGES */);
-  for (int r = found + threadIdx.x; r < want; r += kScanThreads) put(r, -1);
 }
 
 // ws: [0] live pages, [1] moves; then, num_pages of each: the free slot of rank k,

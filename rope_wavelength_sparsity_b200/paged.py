@@ -339,7 +339,8 @@ def pages_free(block_table, refs, rows, lens, page_size: int, *, stream=None):
 
 
 def pages_extend(block_table, refs, rows, lens, new_lens, page_size: int, *, stream=None):
-    """Rows growing from lens[i] to new_lens[i] keys get the pages they lack, lowest free first."""
+    """Rows growing from lens[i] to new_lens[i] keys get the pages they lack, lowest free first; pages
+    that a row holds behind lens[i] (of drafts that were not kept) it grows into."""
     dev, rp, num_pages, tp, num_rows, width = _refs(refs, block_table)
     r = _ints(rows, None, "rows")
     a, b = _ints(lens, len(r), "lens"), _ints(new_lens, len(r), "new_lens")
