@@ -632,8 +632,10 @@ WPATTN_API int wpattn_pages_fork(void *const *pools_host, int32_t n_pools, int32
 
 /*
  * The rows' pages for len[i] keys lose a reference each, and the entries
- * become -1.  An entry outside the pool or a page that is free already:
- * WPATTN_EINDEX recorded.
+ * become -1; so do those behind them, up to the first entry that names no page
+ * (a row that was cut back may hold more pages than its keys need).  A row with
+ * len[i] = 0 is left as it is.  An entry outside the pool before len[i], or a page
+ * that is free already: WPATTN_EINDEX recorded.
  */
 WPATTN_API int wpattn_pages_free(int32_t num_pages, int32_t page_size,
                   int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *refs,

@@ -261,13 +261,16 @@ struct RowsParams {
   int row[MAXN], len[MAXN];
 };
 
-// Block (x, i): row i gives back its pages and its entries become -1.
+// Block (x, i): row i gives back its pages and its entries become -1; the last block
+// of a row goes on to those that it holds behind its length, up to the first
+// entry that names none.  A row of no keys is left as it is.
 template <int MAXN>
 __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ RowsParams<MAXN> p) {
+  __shared__ int stop;
   const int i = blockIdx.y;
   const int pages = (p.len[i] + p.page_size - 1) / p.page_size;
   int32_t* row = p.table + static_cast<int64_t>(p.row[i]) * p.max_pages;
-  for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < pages; j += gridDim.x * blockDim.x) {
+  auto give_back = [&](int j) {
     const int e = row[j];
     row[j] = -1;
     if (e < 0 || e >= p.num_pages) {
@@ -276,6 +279,19 @@ __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ RowsP
       atomicAdd(p.refs + e, 1);           // it was free already
       record_status(6 /* WPATTN_EINDEX */);
     }
+  };
+  for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < pages; j += gridDim.x * blockDim.x) give_back(j);
+  if (blockIdx.x != gridDim.x - 1 || pages == 0) return;
+  for (int j0 = pages; j0 < p.max_pages; j0 += blockDim.x) {
+    const int j = j0 + threadIdx.x;
+    if (threadIdx.x == 0) stop = p.max_pages;
+    __syncthreads();
+    if (j < p.max_pages && (row[j] < 0 || row[j] >= p.num_pages)) atomicMin(&stop, j);
+    __syncthreads();
+    const int end = stop;
+    if (j < end) give_back(j);
+    if (end < j0 + static_cast<int>(blockDim.x)) return;
+    __syncthreads();                      // stop is written again
   }
 }
 

@@ -327,7 +327,8 @@ def pages_fork(pools, block_table, refs, src_rows, dst_rows, lens, *, workspace=
 
 
 def pages_free(block_table, refs, rows, lens, page_size: int, *, stream=None):
-    """The pages of rows holding lens[i] keys lose a reference each; their entries become -1."""
+    """The pages of rows holding lens[i] keys lose a reference each, and those that a row holds behind
+    them (of drafts that were not kept); the entries become -1.  Rows of no keys are left as they are."""
     dev, rp, num_pages, tp, num_rows, width = _refs(refs, block_table)
     r = _ints(rows, None, "rows")
     ln = _ints(lens, len(r), "lens")

@@ -116,3 +116,63 @@ def test_serving_with_rejected_drafts(cuda_dev):
         assert torch.equal(rows.cpu(), x)
     used = table[table >= 0]
     assert len(used.unique()) == len(used) and int(refs.sum()) == len(used)
+
+
+class Ending(Rows):
+    """Rows that end with their kept length."""
+
+    def free(self, rows, lens):
+        for r, n in zip(rows, lens):
+            j, width = 0, self.table.shape[1]
+            while n > 0 and j < width and (j < pages_of(n, self.page) or self.table[r, j] >= 0):
+                self.refs[self.table[r, j]] -= 1
+                self.table[r, j] = -1
+                j += 1
+
+
+@pytest.mark.parametrize("kept", [1, 17, 16, 32, 33])
+def test_free_with_the_kept_length(cuda_dev, kept):
+    """A sequence that ends right after its drafts were rejected gives back their pages too."""
+    page = 16
+    made, table, refs, _ = _cache(page, 1, 64, 1, 700, 3, 600)
+    host = Ending(made, table, refs, page)
+    for rows, a, b in (([0, 2], [0, 0], [kept, 20]), ([0], [kept], [kept + 9000])):   # more pages than a block has threads
+        wp.pages_extend(table, refs, rows, a, b, page)
+        host.extend(rows, a, b)
+    assert wp.device_status() == wp.OK
+    host.check(made, table, refs)
+    wp.pages_free(table, refs, [0], [kept], page)
+    host.free([0], [kept])
+    assert wp.device_status() == wp.OK
+    host.check(made, table, refs)
+    assert int(refs.sum()) == 2 and (table[0] == -1).all()
+
+
+def test_free_up_to_the_last_column(cuda_dev):
+    made, table, refs, _ = _cache(8, 1, 64, 1, 9, 2, 3)
+    wp.pages_extend(table, refs, [0, 1], [0, 0], [24, 24], 8)
+    wp.pages_free(table, refs, [0], [3], 8)      # all three columns; the next row's stay
+    assert wp.device_status() == wp.OK
+    assert table.tolist() == [[-1] * 3, [3, 4, 5]] and refs.tolist() == [0, 0, 0, 1, 1, 1, 0, 0, 0]
+    wp.pages_free(table, refs, [0, 1], [0, 8], 8)   # a row of no keys is left as it is
+    assert wp.device_status() == wp.OK and not refs.any()
+
+
+@pytest.mark.parametrize("rows,width,num_pages", [(5, 9, 60), (300, 30, 12000), (1024, 7, 5000)])
+def test_rows_end_with_their_kept_lengths(cuda_dev, rows, width, num_pages):
+    page = 8
+    rng = random.Random(rows + 1)
+    made, table, refs, _ = _cache(page, 1, 64, 1, num_pages, rows, width)
+    host = Ending(made, table, refs, page)
+    for _ in range(4):
+        new = [rng.randint(0, width * page) for _ in range(rows)]
+        wp.pages_extend(table, refs, range(rows), [0] * rows, new, page)
+        host.extend(range(rows), [0] * rows, new)
+        wp.device_status()                        # some calls run out of pages: then rows hold fewer
+        kept = [rng.randint(0, int((host.table[r] >= 0).sum()) * page) for r in range(rows)]
+        kept = [max(n, 1) if host.table[r, 0] >= 0 else 0 for r, n in enumerate(kept)]
+        wp.pages_free(table, refs, range(rows), kept, page)
+        host.free(range(rows), kept)
+        assert wp.device_status() == wp.OK
+        host.check(made, table, refs)
+        assert not refs.any() and (table == -1).all()
