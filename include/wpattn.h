@@ -621,7 +621,8 @@ WPATTN_API size_t wpattn_pages_workspace_size(int32_t num_pages);
  * are shared, and the begun page's keys (row_bytes each) are copied in every
  * pool into a page of the fork's own.  A row may be the source of any number
  * of forks, but no row both source and destination.  Without enough free pages
- * the last forks' begun pages stay -1 and WPATTN_EPAGES is recorded.
+ * the last forks' begun pages stay -1 and WPATTN_EPAGES is recorded.  A source
+ * entry outside the pool, or of a page that is free: WPATTN_EINDEX recorded.
  */
 WPATTN_API int wpattn_pages_fork(void *const *pools_host, int32_t n_pools, int32_t num_pages,
                   int32_t page_size, int64_t row_bytes,

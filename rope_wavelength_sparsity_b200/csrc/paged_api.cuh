@@ -138,7 +138,12 @@ int launch_fork(const PagePools& pools, int num_pages, int page_size, int64_t ro
     most = std::max(most, len[i] % page_size);
   }
   if (begun > 0) {
-    find_free_pages_kernel<<<1, kScanThreads, 0, st>>>(refs, num_pages, list, begun);
+    ForkSources<MAXN> from;
+    from.table = table;
+    from.num_pages = num_pages; from.max_pages = max_pages; from.page_size = page_size; from.n = n;
+    std::copy(src, src + n, from.src);
+    std::copy(len, len + n, from.len);
+    find_free_pages_kernel<MAXN><<<1 + n, kScanThreads, 0, st>>>(refs, num_pages, list, begun, from);
     const int rc = launched();
     if (rc != WPATTN_OK) return rc;
   }

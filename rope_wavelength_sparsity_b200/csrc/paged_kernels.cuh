@@ -186,10 +186,32 @@ __device__ __forceinline__ void block_copy(uint8_t* __restrict__ dst, const uint
 }
 constexpr int kCopyUnits = 1024;       // 16-byte units (16 KB) of one page that a block copies at a time
 
-// The lowest `want` free pages, in order, into list; -1 where there are fewer.
+// Source rows of a fork, for the look at their pages' refs.
+template <int MAXN>
+struct ForkSources {
+  const int32_t* table;    // [rows, max_pages]
+  int num_pages, max_pages, page_size, n;
+  int src[MAXN], len[MAXN];
+};
+
+// Block 0: the lowest `want` free pages, in order, into list; -1 where there are fewer.
+// The others look at the source rows: a page there that is free may be one of those
+// handed out, which the fork itself, whose blocks raise counts in any order, cannot
+// tell.  Beside the search they take no time of their own.
+template <int MAXN>
 __global__ void __launch_bounds__(kScanThreads)
-find_free_pages_kernel(const int32_t* __restrict__ refs, int num_pages, int32_t* __restrict__ list, int want) {
+find_free_pages_kernel(const int32_t* __restrict__ refs, int num_pages, int32_t* __restrict__ list, int want,
+                       const __grid_constant__ ForkSources<MAXN> p) {
   __shared__ int sums[kScanThreads / 32];
+  for (int f = blockIdx.x - 1; f >= 0 && f < p.n; f += gridDim.x - 1) {
+    const int pages = (p.len[f] + p.page_size - 1) / p.page_size;
+    const int32_t* from = p.table + static_cast<int64_t>(p.src[f]) * p.max_pages;
+    for (int j = threadIdx.x; j < pages; j += kScanThreads) {
+      const int e = from[j];
+      if (e >= 0 && e < num_pages && refs[e] <= 0) record_status(6 /* WPATTN_EINDEX */);
+    }
+  }
+  if (blockIdx.x > 0) return;
   int found = 0;
   for (int base = 0; base < num_pages && found < want; base += kScanThreads) {
     const int i = base + threadIdx.x;
@@ -227,8 +249,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ ForkP
       int e = -1;
       if (j < full) {
         e = from[j];
-        if (e < 0 || e >= p.num_pages) record_status(6 /* WPATTN_EINDEX */);
-        else atomicAdd(p.refs + e, 1);
+        if (e < 0 || e >= p.num_pages || atomicAdd(p.refs + e, 1) <= 0) record_status(6 /* WPATTN_EINDEX */);
       } else if (j == full && part) {
         e = fresh;
         if (e < 0) record_status(7 /* WPATTN_EPAGES */);
