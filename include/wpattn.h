@@ -512,6 +512,14 @@ WPATTN_API int wpattn_merge_lse(const void *outs, const float *lses, int32_t R, 
  *   kv_len_host: host int32 [B], its cached keys, 0 <= kv_len <=
  *                max_pages_per_seq * page_size.  Query t sits at kv_len - q_len
  *                + t, key j at j; one before key 0 gets out = 0, lse = -inf.
+ *                These are the distances that the window and causality go by,
+ *                whatever positions turned the queries and keys: a cache that
+ *                wpattn_append_paged filled by positions of their own is pruned
+ *                by its rows here, where wpattn_decode_paged takes q_pos and
+ *                k_pos.  Where rows run ahead of positions (image and video
+ *                tokens: a frame of 36 x 36 is 1296 rows and one step in time),
+ *                pairs are left out after that much less of their wavelength;
+ *                alpha = +INFINITY leaves none out.
  *   out        : bf16 device [T, Hq, D];  lse: fp32 device [T, Hq] or NULL
  *   workspace  : device, 256-byte aligned, at least
  *                wpattn_prefill_paged_workspace_size(...) bytes (else
@@ -574,7 +582,8 @@ WPATTN_API int wpattn_rope_axes(const void *q, int64_t q_stride, void *q_out,
  *   rope_base  : 0 = the tokens are stored as they are (q, positions and
  *                pair_axis_host NULL); otherwise k and q turn as in
  *                wpattn_rope_axes, by positions (NULL: the token's cache row;
- *                axes = 1)
+ *                axes = 1).  Positions are not kept with the cache:
+ *                wpattn_prefill_paged's window goes by rows whatever they were
  * A table entry outside the pool: the token is not stored and WPATTN_EINDEX
  * recorded.  Nothing else of the pools is written.  B <= 1024; the page sizes
  * of wpattn_decode_paged.

@@ -120,9 +120,10 @@ def prefill_paged(q, k_pages, v_pages, block_table, q_len, kv_len, w: Window, *,
     """Windowed attention of a ragged batch of chunks over a paged cache.
 
     q [T, Hq, D]: the new tokens of each sequence one after another, q_len[b] of them; kv_len[b]
-    counts the sequence's cached keys, the new tokens' among them.  Rows of q behind the last
-    sequence are not read, those of out and lse left as they are.  Returns (out [T, Hq, D] bf16,
-    lse [T, Hq] fp32 or None).
+    counts the sequence's cached keys, the new tokens' among them.  The window goes by the distance
+    of cache rows, also where ``append_paged`` was given other positions (``decode_paged`` takes
+    those; with alpha = inf no distance matters).  Rows of q behind the last sequence are not read,
+    those of out and lse left as they are.  Returns (out [T, Hq, D] bf16, lse [T, Hq] fp32 or None).
     """
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, D]")
@@ -222,8 +223,10 @@ def append_paged(k, v, k_pages, v_pages, block_table, new_len, kv_len, *, q=None
     after another, become rows kv_len[b] - new_len[b] .. kv_len[b] - 1 (kv_len counts them).
 
     With ``base`` k is rotated on the way, and q [T, Hq, D] beside it (returned), as in
-    ``rope_axes`` by ``positions`` and ``pair_axes`` (None: by each token's cache row).  k, v and q
-    may be slices of one projection.  Rows behind the last sequence are neither read nor written.
+    ``rope_axes`` by ``positions`` and ``pair_axes`` (None: by each token's cache row).  Positions
+    are not kept with the cache: ``prefill_paged`` prunes by the distance of rows whatever they
+    were.  k, v and q may be slices of one projection.  Rows behind the last sequence are neither
+    read nor written.
     """
     dev = k.get_device() if isinstance(k, torch.Tensor) else -1
     kp, ks, shape = _tokens(k, "k", dev)
