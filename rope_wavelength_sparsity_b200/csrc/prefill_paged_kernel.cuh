@@ -40,8 +40,11 @@
 // PV and the next QK (1150).  Measured: 3650 cycles a step (4100 with the
 // tiles' exponentials side by side).  At D = 64 the next QK runs early, beside
 // the softmax, and a step is both tiles' softmax passes: 3000 cycles.  4096
-// queries of 28 heads on 128K keys, 4 kv heads, g = 8: 5.55 to 5.9 ms, about
-// 1000 TFLOP/s of kept terms; one query a sequence: 7.0 TB/s of K and V.
+// queries of 28 heads on 128K keys, 4 kv heads, g = 8: 5.55 to 6.3 ms (by GPU
+// and power), 900 to 1000 TFLOP/s of kept terms.  One query in each of 64 sequences
+// of 1000 to 32000 keys (D = 128, 16-key pages, 8 kv heads, g = 1): 677 to 689 us,
+// 6.2 TB/s of K and V; all of 32000 keys (64-key pages, g = 8): 1.21 to 1.26 ms, 6.7
+// to 6.9 TB/s.
 //
 // Shared-memory layouts.  K and V tiles are groups of 8 keys, each D / 64
 // panels of 8 rows x 128 bytes, 128-byte swizzled: the layout one 4-D copy
@@ -992,7 +995,7 @@ prefill_paged_merge_kernel(const __grid_constant__ PrefillPagedParams<MAXB> p) {
   for (int e = 0; e < 32; ++e) acc[e] = 0.f;
   for (int s = 0; s < it.parts; ++s) {
     const float ls = pl[static_cast<size_t>(s) * step * 256];
-    if (ls == -INFINITY) continue;                         // no key: its O was not written
+    if (ls == -INFINITY) continue;                         // no key: weight 0
     const float w = ex2_approx(ls - M);
     W += w;
 #pragma unroll
