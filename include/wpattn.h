@@ -601,7 +601,8 @@ WPATTN_API int wpattn_append_paged(const void *k, int64_t k_stride,
 
 /*
  * Page maintenance.  A cache is a block table [num_rows, max_pages] (device
- * int32, one row per sequence slot, -1 = no page), refs [num_pages] (device
+ * int32, one row per sequence slot, -1 = no page, all of it -1 to begin with:
+ * entries behind a row's keys are taken for pages it holds), refs [num_pages] (device
  * int32: how many table entries name each page, 0 = free) and any number of
  * pools (the K and V pools of every layer, all with the same pages): a host
  * array of up to 256 device pointers, 16-byte aligned, a page being page_bytes
@@ -655,10 +656,10 @@ WPATTN_API int wpattn_pages_free(int32_t num_pages, int32_t page_size,
  * Row i grows from len[i] to new_len[i] keys: the pages it lacks are the lowest
  * free ones, row by row.  An entry behind len[i] that names a page in use keeps
  * it: a row that was cut back (drafts that were not kept) grows into the pages
- * it holds.  (One that names a free page is replaced, and WPATTN_EINDEX
- * recorded.)  Cutting back is the host's: a smaller length, though not below one
- * that the row was forked at, since pages behind that may be shared.  Without
- * enough free pages the last entries stay -1 and WPATTN_EPAGES is recorded.  At
+ * it holds.  Cutting back is the host's: a smaller length, though not below one
+ * that the row was forked at, since pages behind that may be shared.  An entry
+ * behind len[i] of a shared page (it stays) or of a free one (it is replaced):
+ * WPATTN_EINDEX recorded.  Without enough free pages the last entries stay -1 and WPATTN_EPAGES is recorded.  At
  * most 2^30 entries per call, all rows together (else WPATTN_EUNSUPPORTED).
  */
 WPATTN_API int wpattn_pages_extend(int32_t num_pages, int32_t page_size,

@@ -329,13 +329,16 @@ struct ExtendParams {
 // that were not kept).  The threads find those that lack one, up to four entries each
 // a round, and scan two rows of 1024 counts at once (in 16 bits each); then the pool's
 // refs go by, from where the entries before left them.  Bound by the rounds' latency.
-// (64 rows by 500 pages each: 52 us, with one entry a thread and round 65 us; 1000 rows
+// (64 rows by 500 pages each: 55 us, with one entry a thread and round 65 us; 1000 rows
 // by one: 14 us, with four neighbouring entries a thread 19 us.)
 __global__ void __launch_bounds__(kScanThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
   constexpr int kEach = 4;
   __shared__ int sums[kScanThreads / 32];
   __shared__ int32_t* slots[kScanThreads * kEach];   // the entries that lack a page
   const int want = p.start[p.n];
+  // until a call of several rounds ends, a page that it hands out has this count: an entry
+  // that a later round looks at and that names the page is then still told from its owner's
+  const int taken = want > kScanThreads * kEach ? INT32_MIN : 1;
   int base = 0;                              // every page before it is in use
   for (int r0 = 0; r0 < want; r0 += kScanThreads * kEach) {
     int32_t* entry[kEach];
@@ -354,8 +357,9 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const __grid_const
 #pragma unroll
     for (int u = 0; u < kEach; ++u)
       if (lacks[u] && e[u] >= 0 && e[u] < p.num_pages) {
-        lacks[u] = p.refs[e[u]] <= 0;
-        if (lacks[u]) record_status(6 /* WPATTN_EINDEX */);   // a free page
+        const int held = p.refs[e[u]];
+        lacks[u] = held <= 0;
+        if (held != 1) record_status(6 /* WPATTN_EINDEX */);   // a free page, or one that others read
       }
 #pragma unroll
     for (int u = 0; u < kEach; u += 2) {
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const __grid_const
       int found;
       const int k = got + block_scan(free, sums, &found);
       if (free && k < n) {
-        p.refs[page] = 1;
+        p.refs[page] = taken;
         *slots[k] = page;
       }
       if (got + found <= n) base += kScanThreads;   // else the next entries take the rest of these
@@ -384,6 +388,11 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const __grid_const
     for (int k = got + threadIdx.x; k < n; k += kScanThreads) *slots[k] = -1;
     __syncthreads();                         // slots may be reused
   }
+  if (taken == 1) return;
+  const int end = min(base + kScanThreads, p.num_pages);
+#pragma unroll 4
+  for (int page = threadIdx.x; page < end; page += kScanThreads)
+    if (p.refs[page] == taken) p.refs[page] = 1;
 }
 
 // ws: [0] live pages, [1] moves; then, num_pages of each: the free slot of rank k,

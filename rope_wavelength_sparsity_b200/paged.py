@@ -1,9 +1,9 @@
 """Binding of the paged-cache operators: what a serving step does around ``decode_paged``.
 
 A cache is a pair of page pools k_pages, v_pages [num_pages, page_size, Hkv, D] (bf16 CUDA; one
-pair per layer), a block table [rows, max_pages] (int32 CUDA, -1 = no page), refs [num_pages]
-(int32 CUDA, how many table entries name each page) and the sequences' lengths, which the host
-keeps.  A step: ``pages_extend`` for the pages that the new tokens need, ``append_paged`` to
+pair per layer), a block table [rows, max_pages] (int32 CUDA, -1 = no page, all of it -1 to begin
+with), refs [num_pages] (int32 CUDA, how many table entries name each page) and the sequences'
+lengths, which the host keeps.  A step: ``pages_extend`` for the pages that the new tokens need, ``append_paged`` to
 rotate and store them, then ``prefill_paged`` (or ``decode_paged``) to attend; ``pages_fork``,
 ``pages_free``, ``pages_copy`` and ``pages_compact`` tend the pages between steps.
 

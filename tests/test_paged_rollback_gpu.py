@@ -176,3 +176,30 @@ def test_rows_end_with_their_kept_lengths(cuda_dev, rows, width, num_pages):
         assert wp.device_status() == wp.OK
         host.check(made, table, refs)
         assert not refs.any() and (table == -1).all()
+
+
+def test_growing_over_a_shared_page_is_reported(cuda_dev):
+    """A row cut back below a length it was forked at: its tokens would go into pages that the fork reads."""
+    made, table, refs, _ = _cache(8, 1, 64, 1, 9, 3, 4)
+    wp.pages_extend(table, refs, [0], [0], [24], 8)
+    wp.pages_fork(made, table, refs, [0], [1], [24])
+    wp.pages_extend(table, refs, [0], [24], [25], 8)           # both go on from there
+    assert wp.device_status() == wp.OK
+    wp.pages_extend(table, refs, [0], [24], [30], 8)           # a page of its own
+    assert wp.device_status() == wp.OK
+    wp.pages_extend(table, refs, [0], [16], [20], 8)
+    assert wp.device_status() == wp.EINDEX
+    assert table[0].tolist() == [0, 1, 2, 3] and refs.tolist() == [2, 2, 2, 1, 0, 0, 0, 0, 0]
+
+
+def test_entries_of_free_pages_in_a_large_call(cuda_dev):
+    """Several thousand entries: the first rows are given the pages that the last row's entries name."""
+    made, table, refs, _ = _cache(8, 1, 64, 1, 9000, 3, 6000)
+    refs[5] = 1                                  # in use elsewhere
+    table[2, :3] = torch.tensor([7, 8999, 3], dtype=torch.int32)
+    wp.pages_extend(table, refs, [0, 1, 2], [0, 0, 0], [8 * 5000, 8 * 100, 8 * 3], 8)
+    assert wp.device_status() == wp.EINDEX
+    used = table[table >= 0]
+    assert len(used) == 5103 and len(used.unique()) == 5103
+    assert refs.tolist() == [1] * 5104 + [0] * (9000 - 5104)
+    assert table[2, :3].tolist() == [5101, 5102, 5103]
