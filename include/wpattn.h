@@ -659,8 +659,9 @@ WPATTN_API int wpattn_pages_free(int32_t num_pages, int32_t page_size,
  * it holds.  Cutting back is the host's: a smaller length, though not below one
  * that the row was forked at, since pages behind that may be shared.  An entry
  * behind len[i] of a shared page (it stays) or of a free one (it is replaced):
- * WPATTN_EINDEX recorded.  Without enough free pages the last entries stay -1 and WPATTN_EPAGES is recorded.  At
- * most 2^30 entries per call, all rows together (else WPATTN_EUNSUPPORTED).
+ * WPATTN_EINDEX recorded.  Without enough free pages the last entries stay -1
+ * and WPATTN_EPAGES is recorded.  At most 2^30 entries per call, all rows
+ * together (else WPATTN_EUNSUPPORTED).
  */
 WPATTN_API int wpattn_pages_extend(int32_t num_pages, int32_t page_size,
                   int32_t *block_table, int32_t num_rows, int32_t max_pages, int32_t *refs,

@@ -3,9 +3,9 @@
 A cache is a pair of page pools k_pages, v_pages [num_pages, page_size, Hkv, D] (bf16 CUDA; one
 pair per layer), a block table [rows, max_pages] (int32 CUDA, -1 = no page, all of it -1 to begin
 with), refs [num_pages] (int32 CUDA, how many table entries name each page) and the sequences'
-lengths, which the host keeps.  A step: ``pages_extend`` for the pages that the new tokens need, ``append_paged`` to
-rotate and store them, then ``prefill_paged`` (or ``decode_paged``) to attend; ``pages_fork``,
-``pages_free``, ``pages_copy`` and ``pages_compact`` tend the pages between steps.
+lengths, which the host keeps.  A step: ``pages_extend`` for the pages that the new tokens need,
+``append_paged`` to rotate and store them, then ``prefill_paged`` (or ``decode_paged``) to attend;
+``pages_fork``, ``pages_free``, ``pages_copy`` and ``pages_compact`` tend the pages between steps.
 
 Calls run on torch's current stream of the tensors' device, or on ``stream``: what a call
 allocates then belongs to that stream.  Lengths and row numbers are host ints.
